@@ -14,5 +14,7 @@ from .binding import (  # noqa: F401
     launch_count, profile_enable, profile_read, ETOOLARGE, NOALLOC_SCRATCH_BYTES,
     gemm_q2_noalloc, gemm_q2_dual, dual_workspace_size, tc_plan, TC_PLAN_KEYS,
     q2_from_gemlite, PACK_ZERO_MISMATCH, PACK_GROUP_MISMATCH, gemm_q2_lora_bt,
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU, MAX_EXPERTS, expert_combine,
+    expert_sort, gemm_q2_ep, gemm_q2_grouped, gemm_q4_ep, gemm_q4_grouped,
     selftest_wait_timeout, gemv_plan, GEMV_PLAN_KEYS, mma_rate,
 )

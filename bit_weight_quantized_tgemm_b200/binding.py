@@ -25,6 +25,8 @@ PATH_AUTO, PATH_SMALL_M, PATH_TENSOR, PATH_SMALL_M_PASS, PATH_SMALL_M_STREAM = 0
 PACK_BAD_CODE, PACK_INEXACT, PACK_NONFINITE = 1, 2, 4
 PACK_ZERO_MISMATCH, PACK_GROUP_MISMATCH = 8, 16
 DEVERR_TIMEOUT = 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
+MAX_EXPERTS = 1024
 KIND_TC_Q2, KIND_TC_Q2_LORA, KIND_TC_Q4, KIND_GEMV_Q2, KIND_GEMV_Q4, KIND_PREP = range(6)
 
 _P = ctypes.c_void_p
@@ -52,6 +54,15 @@ _SIGS = {
     "tgemm_q4": (_i, [_P, _P, _P, _P, _i, _i, _i, _i, _P, _sz, _P]),
     "tgemm_q2_dual": (_i, [_P, _P, _P, _i, _P, _P, _P, _i, _P, _i, _i, _i, _P, _sz, _P]),
     "tgemm_q2_noalloc": (_i, [_P, _P, _P, _P, _i, _i, _i, _i, _P]),
+    "tgemm_q2_ep": (_i, [_P, _P, _P, _P, _P, _i, _i, _i, _i, _P, _sz, _P]),
+    "tgemm_q4_ep": (_i, [_P, _P, _P, _P, _P, _i, _i, _i, _i, _P, _sz, _P]),
+    "tgemm_ep_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "tgemm_q2_grouped": (_i, [_P, _i, _P, _P, _P, _P, _P, _P, _i, _i, _i, _i, _i, _P, _sz, _P]),
+    "tgemm_q4_grouped": (_i, [_P, _i, _P, _P, _P, _P, _P, _P, _i, _i, _i, _i, _i, _P, _sz, _P]),
+    "tgemm_grouped_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "tgemm_expert_sort": (_i, [_P, _i, _i, _i, _P, _P, _P, _P, _sz, _P]),
+    "tgemm_expert_sort_workspace_size": (_sz, [_i, _i, _i]),
+    "tgemm_expert_combine": (_i, [_P, _i, _P, _P, _P, _i, _P, _i, _i, _i, _i, _i, _P]),
     "tgemm_strerror": (ctypes.c_char_p, [_i]),
     "tgemm_set_path": (_i, [_i]),
     "tgemm_device_error": (_i, [_P, _i]),
@@ -381,6 +392,200 @@ def gemm_q4(x, wq, sz, *, out_dtype: int = OUT_BF16, y=None, workspace=None):
     ws, nbytes = _workspace(OP_Q4, M, N, K, 0, x.device, workspace)
     _check(lib().tgemm_q4(_ptr(x), _ptr(wq), _ptr(sz), _ptr(y), M, N, K, out_dtype, _ptr(ws),
                           nbytes, _stream()), "tgemm_q4")
+    return y
+
+
+# ---- matmuls with an epilogue, and grouped by expert --------------------------------------------
+
+class _Epilogue(ctypes.Structure):
+    """tgemm_epilogue of tgemm.h."""
+    _fields_ = [("bias", _P), ("gate", _P), ("residual", _P), ("bias_dtype", _i), ("act", _i),
+                ("gate_rows", _i), ("residual_dtype", _i)]
+
+
+def _out_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return OUT_F32
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+
+
+def _shape(t: torch.Tensor, shape, name: str):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _epilogue(bias, act, gate, residual, M, N, E=None) -> _Epilogue:
+    """Checks the epilogue's tensors and fills the C struct; E is set for grouped calls."""
+    ep = _Epilogue(act=act)
+    if bias is not None:
+        ep.bias_dtype = _out_code(bias, "bias")
+        _need(bias, bias.dtype, "bias")
+        _shape(bias, (N,) if E is None else (E, N), "bias")
+        ep.bias = _ptr(bias)
+    if gate is not None:
+        _need(gate, torch.bfloat16, "gate")
+        ep.gate_rows = 0 if E is None and gate.dim() == 1 else 1
+        _shape(gate, (M, N) if ep.gate_rows else (N,), "gate")
+        ep.gate = _ptr(gate)
+    if residual is not None:
+        ep.residual_dtype = _out_code(residual, "residual")
+        _need(residual, residual.dtype, "residual")
+        _shape(residual, (M, N), "residual")
+        ep.residual = _ptr(residual)
+    return ep
+
+
+def _one_device(*tensors):
+    """The device all the given tensors are on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _call_workspace(need: int, workspace, device):
+    """The caller's workspace, or one of this call's own: the allocator gives it to no other
+    stream or captured graph while this call may still use it."""
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+        return workspace, workspace.numel()
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, y, workspace):
+    _need(x, torch.bfloat16, "x")
+    _need(wq, torch.uint8, "wq")
+    _need(sc, torch.float16, "scales")
+    if x.dim() != 2 or wq.dim() != 2:
+        raise ValueError("x and wq must have two dimensions")
+    M, K = x.shape
+    N = wq.shape[0]
+    _shape(wq, (N, K // per_byte), "wq")
+    _shape(sc, (N, K // 128) if per_byte == 4 else (N, K // 64, 2), "scales")
+    ep = _epilogue(bias, act, gate, residual, M, N)
+    device = _one_device(x, wq, sc, bias, gate, residual, y, workspace)
+    with torch.cuda.device(device):
+        y = _out(y, M, N, out_dtype, device)
+        ws, nbytes = _call_workspace(int(lib().tgemm_ep_workspace_size(op, M, N, K)), workspace, device)
+        _check(getattr(lib(), fn)(_ptr(x), _ptr(wq), _ptr(sc), ctypes.addressof(ep), _ptr(y), M, N, K,
+                                  out_dtype, _ptr(ws), nbytes, _stream()), fn)
+    return y
+
+
+def gemm_q2_ep(x, wq, d, *, bias=None, act: int = ACT_NONE, gate=None, residual=None,
+               out_dtype: int = OUT_BF16, y=None, workspace=None):
+    """y = residual + gate * act(x . W^T + bias), W packed Q2_0 (wq uint8 [N, K/4], d f16 [N, K/128]).
+
+    bias f32 or bf16 [N]; act ACT_*; gate bf16 [N] or [M, N]; residual f32 or bf16 [M, N].  The
+    epilogue is f32 with one rounding, at the store.  y may be the residual (of y's type) or a
+    bf16 [M, N] gate.  See tgemm_epilogue in tgemm.h."""
+    return _gemm_ep("tgemm_q2_ep", OP_Q2, x, wq, d, 4, bias, act, gate, residual, out_dtype, y, workspace)
+
+
+def gemm_q4_ep(x, wq, sz, *, bias=None, act: int = ACT_NONE, gate=None, residual=None,
+               out_dtype: int = OUT_BF16, y=None, workspace=None):
+    """gemm_q2_ep for 4-bit weights (wq uint8 [N, K/2], sz f16 [N, K/64, 2])."""
+    return _gemm_ep("tgemm_q4_ep", OP_Q4, x, wq, sz, 2, bias, act, gate, residual, out_dtype, y, workspace)
+
+
+def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, residual, out_dtype, y, workspace):
+    _need(x, torch.bfloat16, "x")
+    _need(wq, torch.uint8, "wq")
+    _need(sc, torch.float16, "scales")
+    _need(offsets, torch.int32, "offsets")
+    if x.dim() != 2 or wq.dim() != 3:
+        raise ValueError("x must have two dimensions and wq three")
+    x_rows, K = x.shape
+    E, N = wq.shape[:2]
+    _shape(wq, (E, N, K // per_byte), "wq")
+    _shape(sc, (E, N, K // 128) if per_byte == 4 else (E, N, K // 64, 2), "scales")
+    _shape(offsets, (E + 1,), "offsets")
+    R = x_rows
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.dim() != 1:
+            raise ValueError("rows must have one dimension")
+        R = rows.shape[0]
+    ep = _epilogue(bias, act, gate, residual, R, N, E)
+    device = _one_device(x, wq, sc, offsets, rows, bias, gate, residual, y, workspace)
+    with torch.cuda.device(device):
+        y = _out(y, R, N, out_dtype, device)
+        ws, nbytes = _call_workspace(int(lib().tgemm_grouped_workspace_size(op, R, E, N, K)), workspace, device)
+        _check(getattr(lib(), fn)(_ptr(x), x_rows, _ptr(wq), _ptr(sc), _ptr(offsets), _ptr(rows),
+                                  ctypes.addressof(ep), _ptr(y), R, E, N, K, out_dtype, _ptr(ws), nbytes,
+                                  _stream()), fn)
+    return y
+
+
+def gemm_q2_grouped(x, wq, d, offsets, *, rows=None, bias=None, act: int = ACT_NONE, gate=None,
+                    residual=None, out_dtype: int = OUT_BF16, y=None, workspace=None):
+    """Matmul grouped by expert, Q2_0 weights: rows [offsets[e], offsets[e+1]) of y are
+    residual + gate * act(xs . W_e^T + bias[e]), xs = x[rows] (or x).
+
+    wq uint8 [E, N, K/4], d f16 [E, N, K/128], offsets int32 [E+1] on the device (as expert_sort
+    gives them), rows int32 [R]; bias [E, N], gate bf16 [R, N], residual [R, N].  Rows of y behind
+    the last group are left as they were.  See tgemm_q2_grouped in tgemm.h."""
+    return _gemm_grouped("tgemm_q2_grouped", OP_Q2, x, wq, d, 4, offsets, rows, bias, act, gate, residual,
+                         out_dtype, y, workspace)
+
+
+def gemm_q4_grouped(x, wq, sz, offsets, *, rows=None, bias=None, act: int = ACT_NONE, gate=None,
+                    residual=None, out_dtype: int = OUT_BF16, y=None, workspace=None):
+    """gemm_q2_grouped for 4-bit weights (wq uint8 [E, N, K/2], sz f16 [E, N, K/64, 2])."""
+    return _gemm_grouped("tgemm_q4_grouped", OP_Q4, x, wq, sz, 2, offsets, rows, bias, act, gate, residual,
+                         out_dtype, y, workspace)
+
+
+def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
+    """The plan of a grouped matmul from ids int32 [T, k] (the experts of each token).
+
+    Returns (offsets int32 [experts+1], rows int32 [T*k], pos int32 [T, k]): expert e's sorted
+    rows are [offsets[e], offsets[e+1]), rows[r] is the token of sorted row r (-1 behind the
+    last), pos[t, j] the sorted row of pair (t, j) (-1 for an id outside [0, experts), whose pair
+    is left out).  Pairs of one expert keep their order."""
+    _need(ids, torch.int32, "ids")
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    T, k = ids.shape
+    device = _one_device(ids, workspace)
+    with torch.cuda.device(device):
+        offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=device)
+        rows = torch.empty(T * k, dtype=torch.int32, device=device)
+        pos = torch.empty((T, k), dtype=torch.int32, device=device)
+        ws, nbytes = _call_workspace(int(lib().tgemm_expert_sort_workspace_size(T, k, experts)), workspace, device)
+        _check(lib().tgemm_expert_sort(_ptr(ids), T, k, experts, _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(ws),
+                                       nbytes, _stream()), "tgemm_expert_sort")
+    return offsets, rows, pos
+
+
+def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *, residual=None,
+                   out_dtype: int = OUT_BF16, y=None):
+    """y[t] = residual[t] + sum_j weights[t, j] * h[pos[t, j]] (pairs with pos outside [0, R) left
+    out): h f32 or bf16 [R, N], pos int32 [T, k], weights f32 [T, k], residual f32 or bf16 [T, N].
+    f32 sums in the order of j."""
+    hd = _out_code(h, "h")
+    _need(h, h.dtype, "h")
+    _need(pos, torch.int32, "pos")
+    _need(weights, torch.float32, "weights")
+    if h.dim() != 2 or pos.dim() != 2:
+        raise ValueError("h must be [R, N] and pos [T, k]")
+    T, k = pos.shape
+    R, N = h.shape
+    _shape(weights, (T, k), "weights")
+    rd = 0
+    if residual is not None:
+        rd = _out_code(residual, "residual")
+        _need(residual, residual.dtype, "residual")
+        _shape(residual, (T, N), "residual")
+    device = _one_device(h, pos, weights, residual, y)
+    with torch.cuda.device(device):
+        y = _out(y, T, N, out_dtype, device)
+        _check(lib().tgemm_expert_combine(_ptr(h), hd, _ptr(pos), _ptr(weights), _ptr(residual), rd, _ptr(y),
+                                          T, k, N, R, out_dtype, _stream()), "tgemm_expert_combine")
     return y
 
 

@@ -1,0 +1,269 @@
+// ep_host.cuh -- host side of the epilogue and expert matmuls, the expert sort and combine:
+// argument checks, workspace layout, dispatch.  Part of tgemm.cu (uses its launch helpers).
+#pragma once
+
+namespace tgemm {
+namespace {
+
+// [a, a + na) and [b, b + nb) share a byte.
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+struct EpCall {
+  int fmt;
+  const uint16_t* x;
+  const uint8_t* wq;
+  const uint16_t* scales;
+  const int* offsets;  // null: dense
+  const int* rows;
+  int E, x_rows, R, N, K;
+  const tgemm_epilogue* ep;
+  void* y;
+  int out_dtype;
+  void* workspace;
+  size_t ws_bytes;
+  void* stream;
+};
+
+bool dtype_ok(int dt) { return dt == TGEMM_OUT_F32 || dt == TGEMM_OUT_BF16; }
+
+// Bytes of the f16 copy of the activations (tensor-core path).
+size_t ep_x16_bytes(int R, int K) { return round_up(static_cast<size_t>(R) * K * 2, 256); }
+
+// Tokens per tile of a dense call: the candidate whose fullest CTA has the least to do.  A
+// 128-k stage costs 4 cycles per token on the tensor core and no less than the dequantizers
+// need for its 128 x 128 weights.
+int et_pick_nt(int M, int tiles_n, int sms) {
+  int best = kEtTok;
+  int64_t best_cost = INT64_MAX;
+  for (int nt = 16; nt <= kEtTok; nt += 16) {
+    const int64_t tiles = static_cast<int64_t>((M + nt - 1) / nt) * tiles_n;
+    const int64_t cost = (tiles + sms - 1) / sms * std::max(4 * nt, 350);
+    if (cost <= best_cost) {
+      best_cost = cost;
+      best = nt;
+    }
+  }
+  return best;
+}
+
+template <int FMT, bool SPLIT>
+int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(ep_tc_kernel<FMT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               EtFmt<FMT>::kSmemBytes);
+  });
+  if (err != cudaSuccess) return TGEMM_ECUDA;
+  CUtensorMap tm_x128, tm_x16, tm_w;
+  const uint64_t rows = static_cast<uint64_t>(c.R);
+  if (int e = make_map_2d(&tm_x128, c.workspace, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.K, rows, 64, kEtTok,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  if (int e = make_map_2d(&tm_x16, c.workspace, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.K, rows, 64, 16,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+    return e;
+  const uint64_t row_bytes = static_cast<uint64_t>(c.K) / (FMT == 0 ? 4 : 2);
+  if (int e = make_map_2d(&tm_w, c.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row_bytes,
+                          static_cast<uint64_t>(c.E) * c.N, EtFmt<FMT>::kWqRowBytes, kEtRows,
+                          FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return e;
+  return launch(FMT == 0 ? TGEMM_KIND_TC_Q2 : TGEMM_KIND_TC_Q4, st, [&] {
+    return pdl_launch(ep_tc_kernel<FMT, SPLIT>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm_x128, tm_x16,
+                      tm_w, p);
+  });
+}
+
+int run_ep(const EpCall& c) {
+  const int kblock = c.fmt == 0 ? 128 : 64;
+  if (!c.x || !c.wq || !c.scales || !c.y) return TGEMM_EINVAL;
+  if (c.R < 1 || c.x_rows < 1 || c.N < 1 || c.K < kblock || c.K % kblock) return TGEMM_EINVAL;
+  if (c.E < 1 || c.E > kEtMaxExperts) return TGEMM_EINVAL;
+  if (static_cast<int64_t>(c.E) * c.N > INT32_MAX - kEtRows) return TGEMM_ETOOLARGE;
+  if (!dtype_ok(c.out_dtype)) return TGEMM_EINVAL;
+  if (!aligned(c.x, 16) || !aligned(c.wq, 16) || !aligned(c.y, 16)) return TGEMM_EALIGN;
+  if (!aligned(c.scales, c.fmt == 0 ? 2 : 4)) return TGEMM_EALIGN;
+  if (!aligned(c.offsets, 4) || !aligned(c.rows, 4)) return TGEMM_EALIGN;
+  const int out_f32 = c.out_dtype == TGEMM_OUT_F32 ? 1 : 0;
+  EpArgs a = {};
+  a.y = c.y;
+  a.out_f32 = out_f32;
+  const size_t outs = static_cast<size_t>(c.R) * c.N;
+  const size_t y_bytes = outs * (out_f32 ? 4 : 2);
+  if (c.ep) {
+    const tgemm_epilogue& e = *c.ep;
+    if (e.act < TGEMM_ACT_NONE || e.act > TGEMM_ACT_RELU) return TGEMM_EINVAL;
+    if (e.bias && !dtype_ok(e.bias_dtype)) return TGEMM_EINVAL;
+    if (e.residual && !dtype_ok(e.residual_dtype)) return TGEMM_EINVAL;
+    if (e.gate && e.gate_rows != 0 && e.gate_rows != 1) return TGEMM_EINVAL;
+    if (e.gate && !e.gate_rows && c.offsets) return TGEMM_EINVAL;
+    a.bias = e.bias;
+    a.bias_f32 = e.bias_dtype == TGEMM_OUT_F32;
+    a.act = e.act;
+    a.gate = e.gate;
+    a.gate_rows = e.gate_rows;
+    a.residual = e.residual;
+    a.residual_f32 = e.residual_dtype == TGEMM_OUT_F32;
+    if (!aligned(e.bias, a.bias_f32 ? 4 : 2) || !aligned(e.gate, 16) || !aligned(e.residual, 16)) return TGEMM_EALIGN;
+    // y may be the residual or the gate (the same elements), but not a part of one
+    const size_t res_bytes = outs * (a.residual_f32 ? 4 : 2);
+    if (overlaps(c.y, y_bytes, e.residual, e.residual ? res_bytes : 0) &&
+        !(e.residual == c.y && a.residual_f32 == out_f32))
+      return TGEMM_EINVAL;
+    if (overlaps(c.y, y_bytes, e.gate, e.gate ? (e.gate_rows ? outs : c.N) * 2 : 0) &&
+        !(static_cast<const void*>(e.gate) == c.y && e.gate_rows && !out_f32))
+      return TGEMM_EINVAL;
+    if (overlaps(c.y, y_bytes, e.bias, e.bias ? static_cast<size_t>(c.E) * c.N * (a.bias_f32 ? 4 : 2) : 0))
+      return TGEMM_EINVAL;
+  }
+  const size_t wrows = static_cast<size_t>(c.E) * c.N;
+  if (overlaps(c.y, y_bytes, c.x, static_cast<size_t>(c.x_rows) * c.K * 2) ||
+      overlaps(c.y, y_bytes, c.wq, wrows * (c.K / (c.fmt == 0 ? 4 : 2))) ||
+      overlaps(c.y, y_bytes, c.scales, wrows * (c.fmt == 0 ? c.K / 128 * 2 : c.K / 64 * 4)) ||
+      overlaps(c.y, y_bytes, c.offsets, c.offsets ? (static_cast<size_t>(c.E) + 1) * 4 : 0) ||
+      overlaps(c.y, y_bytes, c.rows, c.rows ? static_cast<size_t>(c.R) * 4 : 0))
+    return TGEMM_EINVAL;
+  const size_t need = ep_x16_bytes(c.R, c.K);
+  if (!c.workspace || c.ws_bytes < need) return TGEMM_EWORKSPACE;
+  if (!aligned(c.workspace, 256)) return TGEMM_EALIGN;
+  if (overlaps(c.y, y_bytes, c.workspace, need)) return TGEMM_EINVAL;
+  DeviceInfo di;
+  if (int e = current_device_info(&di)) return e;
+  const cudaStream_t st = as_stream(c.stream);
+
+  uint16_t* x16 = static_cast<uint16_t*>(c.workspace);
+  const int pgrid = grid_for(static_cast<int64_t>(c.R) * (c.K / 16), 256, di.sms);
+  if (int e = launch(TGEMM_KIND_PREP, st, [&] {
+        if (c.fmt == 0)
+          return pdl_launch(ep_prep_kernel<0>, pgrid, 256, 0, st, c.x, x16, c.rows, c.offsets, c.E, c.x_rows, c.R, c.K);
+        return pdl_launch(ep_prep_kernel<1>, pgrid, 256, 0, st, c.x, x16, c.rows, c.offsets, c.E, c.x_rows, c.R, c.K);
+      }))
+    return e;
+
+  const bool split = c.fmt == 1 && out_f32;
+  EtParams p = {};
+  p.N = c.N;
+  p.K = c.K;
+  p.E = c.E;
+  p.R = c.R;
+  p.tiles_n = (c.N + kEtRows - 1) / kEtRows;
+  p.nt = c.offsets ? kEtTok : et_pick_nt(c.R, p.tiles_n, di.sms);
+  p.ksteps = (c.K + kEtBK - 1) / kEtBK * (split ? 2 : 1);
+  p.offsets = c.offsets;
+  p.scales = c.scales;
+  p.ep = a;
+  // the most tiles there can be: an expert with rows has at most one partly filled tile
+  int64_t tiles = c.R / p.nt + std::min(c.R, c.E);
+  tiles = std::min<int64_t>(tiles, c.R) * p.tiles_n;
+  if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sms));
+  if (c.fmt == 0) return launch_ep_tc<0, false>(c, p, grid, st);
+  return split ? launch_ep_tc<1, true>(c, p, grid, st) : launch_ep_tc<1, false>(c, p, grid, st);
+}
+
+// ---- expert sort and combine ---------------------------------------------------------------
+
+constexpr int64_t kSortMaxPairs = int64_t{1} << 26;
+constexpr int kSortOneCta = 4096;  // pairs one CTA sorts alone
+
+int sort_grid(int64_t n) {
+  if (n <= kSortOneCta) return 1;
+  int64_t g = (n + 4095) / 4096;
+  return static_cast<int>(g > 128 ? 128 : g);
+}
+
+size_t sort_workspace(int64_t n, int E) {
+  const int G = sort_grid(n);
+  return G > 1 ? round_up(static_cast<size_t>(G) * E * 4, 256) : 0;
+}
+
+int run_sort(const int* ids, int T, int k, int E, int* offsets, int* rows, int* pos, void* workspace,
+             size_t ws_bytes, void* stream) {
+  if (!ids || !offsets || !rows || !pos) return TGEMM_EINVAL;
+  if (T < 1 || k < 1 || E < 1 || E > kEtMaxExperts) return TGEMM_EINVAL;
+  const int64_t n = static_cast<int64_t>(T) * k;
+  if (n > kSortMaxPairs) return TGEMM_ETOOLARGE;
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(pos, 4)) return TGEMM_EALIGN;
+  const size_t nb = static_cast<size_t>(n) * 4, ob = (static_cast<size_t>(E) + 1) * 4;
+  if (overlaps(rows, nb, ids, nb) || overlaps(pos, nb, ids, nb) || overlaps(offsets, ob, ids, nb) ||
+      overlaps(rows, nb, pos, nb) || overlaps(rows, nb, offsets, ob) || overlaps(pos, nb, offsets, ob))
+    return TGEMM_EINVAL;
+  const size_t need = sort_workspace(n, E);
+  if (need && (!workspace || ws_bytes < need)) return TGEMM_EWORKSPACE;
+  if (need && !aligned(workspace, 256)) return TGEMM_EALIGN;
+  DeviceInfo di;
+  if (int e = current_device_info(&di)) return e;
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (kSortWarps * kEtMaxExperts + 1) * 4);
+  });
+  if (err != cudaSuccess) return TGEMM_ECUDA;
+  const cudaStream_t st = as_stream(stream);
+  const int G = sort_grid(n);
+  SortParams p;
+  p.ids = ids;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.pos = pos;
+  p.hist = G > 1 ? static_cast<int*>(workspace) : nullptr;
+  p.n = static_cast<int>(n);
+  p.k = k;
+  p.E = E;
+  const int64_t runs = static_cast<int64_t>(G) * kSortWarps;
+  p.run = static_cast<int>(((n + runs - 1) / runs + 31) / 32 * 32);
+  if (G > 1) {
+    if (int e = launch(TGEMM_KIND_PREP, st, [&] {
+          return pdl_launch(sort_count_kernel, G, kSortWarps * 32, static_cast<size_t>(E) * 4, st, p);
+        }))
+      return e;
+  }
+  return launch(TGEMM_KIND_PREP, st, [&] {
+    return pdl_launch(sort_place_kernel, G, kSortWarps * 32, (static_cast<size_t>(kSortWarps) * E + 1) * 4, st, p);
+  });
+}
+
+int run_combine(const void* h, int h_dtype, const int* pos, const float* weights, const void* residual,
+                int residual_dtype, void* y, int T, int k, int N, int R, int out_dtype, void* stream) {
+  if (!h || !pos || !weights || !y) return TGEMM_EINVAL;
+  if (T < 1 || k < 1 || N < 1 || R < 1) return TGEMM_EINVAL;
+  if (!dtype_ok(h_dtype) || !dtype_ok(out_dtype) || (residual && !dtype_ok(residual_dtype))) return TGEMM_EINVAL;
+  if (!aligned(h, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(pos, 4) || !aligned(weights, 4))
+    return TGEMM_EALIGN;
+  const size_t outs = static_cast<size_t>(T) * N;
+  const size_t y_bytes = outs * (out_dtype == TGEMM_OUT_F32 ? 4 : 2);
+  const size_t pairs = static_cast<size_t>(T) * k * 4;
+  if (overlaps(y, y_bytes, h, static_cast<size_t>(R) * N * (h_dtype == TGEMM_OUT_F32 ? 4 : 2)) ||
+      overlaps(y, y_bytes, pos, pairs) || overlaps(y, y_bytes, weights, pairs))
+    return TGEMM_EINVAL;
+  if (residual && overlaps(y, y_bytes, residual, outs * (residual_dtype == TGEMM_OUT_F32 ? 4 : 2)) &&
+      !(residual == y && residual_dtype == out_dtype))
+    return TGEMM_EINVAL;
+  DeviceInfo di;
+  if (int e = current_device_info(&di)) return e;
+  CombineParams p;
+  p.h = h;
+  p.pos = pos;
+  p.weights = weights;
+  p.residual = residual;
+  p.y = y;
+  p.T = T;
+  p.k = k;
+  p.N = N;
+  p.R = R;
+  p.residual_f32 = residual_dtype == TGEMM_OUT_F32;
+  p.out_f32 = out_dtype == TGEMM_OUT_F32;
+  const cudaStream_t st = as_stream(stream);
+  const int grid = grid_for(static_cast<int64_t>(T) * N, 256, di.sms);
+  return launch(TGEMM_KIND_PREP, st, [&] {
+    if (h_dtype == TGEMM_OUT_F32) return pdl_launch(combine_kernel<true>, grid, 256, 0, st, p);
+    return pdl_launch(combine_kernel<false>, grid, 256, 0, st, p);
+  });
+}
+
+}  // namespace
+}  // namespace tgemm

@@ -4,6 +4,7 @@
 // sees the same device error word.  Built for sm_100a only.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstdio>
@@ -19,6 +20,8 @@
 #include "gemv_stream.cuh"
 #include "mma_rate.cuh"
 #include "pack.cuh"
+#include "ep_tc.cuh"
+#include "expert.cuh"
 
 namespace tgemm {
 namespace {
@@ -822,6 +825,8 @@ int noalloc_scratch(void** out) {
 }  // namespace
 }  // namespace tgemm
 
+#include "ep_host.cuh"
+
 using namespace tgemm;
 
 extern "C" {
@@ -1065,6 +1070,56 @@ int tgemm_q4(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, void* y, 
                   stream);
 }
 
+size_t tgemm_ep_workspace_size(int op, int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1 || (op != TGEMM_OP_Q2 && op != TGEMM_OP_Q4)) return 0;
+  return ep_x16_bytes(M, K);
+}
+
+size_t tgemm_grouped_workspace_size(int op, int R, int E, int N, int K) {
+  if (R < 1 || E < 1 || E > TGEMM_MAX_EXPERTS || N < 1 || K < 1 || (op != TGEMM_OP_Q2 && op != TGEMM_OP_Q4))
+    return 0;
+  return ep_x16_bytes(R, K);
+}
+
+int tgemm_q2_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* d, const tgemm_epilogue* ep, void* y, int M,
+                int N, int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  return run_ep(EpCall{0, x, wq, d, nullptr, nullptr, 1, M, M, N, K, ep, y, out_dtype, workspace, ws_bytes, stream});
+}
+
+int tgemm_q4_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, const tgemm_epilogue* ep, void* y, int M,
+                int N, int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  return run_ep(EpCall{1, x, wq, sz, nullptr, nullptr, 1, M, M, N, K, ep, y, out_dtype, workspace, ws_bytes, stream});
+}
+
+int tgemm_q2_grouped(const uint16_t* x, int x_rows, const uint8_t* wq, const uint16_t* d, const int32_t* offsets,
+                     const int32_t* rows, const tgemm_epilogue* ep, void* y, int R, int E, int N, int K,
+                     int out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!offsets || (!rows && x_rows != R)) return TGEMM_EINVAL;
+  return run_ep(EpCall{0, x, wq, d, offsets, rows, E, x_rows, R, N, K, ep, y, out_dtype, workspace, ws_bytes, stream});
+}
+
+int tgemm_q4_grouped(const uint16_t* x, int x_rows, const uint8_t* wq, const uint16_t* sz, const int32_t* offsets,
+                     const int32_t* rows, const tgemm_epilogue* ep, void* y, int R, int E, int N, int K,
+                     int out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!offsets || (!rows && x_rows != R)) return TGEMM_EINVAL;
+  return run_ep(EpCall{1, x, wq, sz, offsets, rows, E, x_rows, R, N, K, ep, y, out_dtype, workspace, ws_bytes, stream});
+}
+
+size_t tgemm_expert_sort_workspace_size(int T, int k, int E) {
+  if (T < 1 || k < 1 || E < 1 || E > TGEMM_MAX_EXPERTS) return 0;
+  return sort_workspace(static_cast<int64_t>(T) * k, E);
+}
+
+int tgemm_expert_sort(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  return run_sort(ids, T, k, E, offsets, rows, pos, workspace, ws_bytes, stream);
+}
+
+int tgemm_expert_combine(const void* h, int h_dtype, const int32_t* pos, const float* weights, const void* residual,
+                         int residual_dtype, void* y, int T, int k, int N, int R, int out_dtype, void* stream) {
+  return run_combine(h, h_dtype, pos, weights, residual, residual_dtype, y, T, k, N, R, out_dtype, stream);
+}
+
 const char* tgemm_strerror(int status) {
   switch (status) {
     case TGEMM_OK: return "success";
@@ -1098,7 +1153,7 @@ int tgemm_device_error(uint32_t* bits, int clear) {
   return TGEMM_OK;
 }
 
-int tgemm_version(void) { return 100; }
+int tgemm_version(void) { return 200; }
 
 int tgemm_profile_enable(int kinds) { return g_profile.exchange(kinds & TGEMM_PROFILE_ALL); }
 

@@ -347,6 +347,110 @@ size_t tgemm_q2_dual_workspace_size_min(int M, int N, int K1, int K2);
 int tgemm_q4(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, void* y, int M, int N,
              int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- epilogue and expert matmuls ------------------------------------------------------- */
+/* Activation of an epilogue. */
+#define TGEMM_ACT_NONE      0
+#define TGEMM_ACT_SILU      1 /* v / (1 + exp(-v)) */
+#define TGEMM_ACT_GELU      2 /* v (1 + erf(v / sqrt 2)) / 2 */
+#define TGEMM_ACT_GELU_TANH 3 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+#define TGEMM_ACT_RELU      4 /* max(v, 0) */
+
+/*
+ * tgemm_epilogue -- what follows a product v = x . W^T before y is stored:
+ *   y[m][n] = residual[m][n] + gate * act(v[m][n] + bias[n])
+ * in f32, rounded once when y is bf16.  A null pointer leaves its term out.
+ *   bias      [N] (grouped calls: [E][N], the row's expert), f32 or bf16 by bias_dtype
+ *             (TGEMM_OUT_*; 4- or 2-byte aligned)
+ *   act       TGEMM_ACT_*
+ *   gate      bf16 (16-byte aligned): gate[n] for every token when gate_rows is 0 (an
+ *             adaptive layer norm's gate; not in grouped calls), gate[m][n] when it is 1
+ *             (the other half of a gated MLP)
+ *   residual  [M][N], f32 or bf16 by residual_dtype (16-byte aligned)
+ * y may be the very tensor that residual is (of y's type), or that a bf16 gate[m][n] is; any
+ * other overlap of y with an input or the workspace is refused (TGEMM_EINVAL).
+ */
+typedef struct tgemm_epilogue {
+  const void* bias;
+  const uint16_t* gate;
+  const void* residual;
+  int bias_dtype;
+  int act;
+  int gate_rows;
+  int residual_dtype;
+} tgemm_epilogue;
+
+/*
+ * tgemm_q2_ep, tgemm_q4_ep -- tgemm_q2 / tgemm_q4 with an epilogue (ep may be null: none).
+ *   Operands, layouts and alignments as tgemm_q2 and tgemm_q4.  x must be finite with
+ *   |x| < 65504.  Every scale is f32-applied or exact in the product's operands: a bf16 y of
+ *   4-bit weights takes W as the f16 rounding of (q - z) * s, an f32 y takes it to f32.
+ *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned; the call
+ *   overwrites it, and calls sharing a workspace must not overlap on the GPU.
+ *   wq and the scales are read before the wait for the kernels ahead on the stream, under
+ *   the same rule as tgemm_q2; x, bias, gate and residual are read after it.
+ */
+int tgemm_q2_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* d, const tgemm_epilogue* ep, void* y, int M,
+                int N, int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+int tgemm_q4_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, const tgemm_epilogue* ep, void* y, int M,
+                int N, int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+size_t tgemm_ep_workspace_size(int op, int M, int N, int K);
+
+/*
+ * tgemm_q2_grouped, tgemm_q4_grouped -- matmuls grouped by expert, with the same epilogue:
+ *   for every expert e and row m of [offsets[e], offsets[e + 1]):
+ *     y[m] = residual[m] + gate[m] * act(xs[m] . W_e^T + bias_e),  xs[m] = x[rows ? rows[m] : m]
+ *   wq, scales  the experts' packed matrices one after another: [E][N][...] as tgemm_q2 / q4
+ *   offsets     int32 [E + 1] on the device (4-byte aligned), non-decreasing, within [0, R].
+ *               It is read on the device, so a call may be captured in a graph and replayed
+ *               with other group sizes.  An expert may have no rows.  Offsets that are not
+ *               so are clamped to [previous, R]: the rows of y are then unspecified, but
+ *               nothing outside the buffers is touched.
+ *   rows        int32 [R] on the device, the row of x for each sorted row, or null (x_rows
+ *               must then be R).  An index outside [0, x_rows) reads a row of zeros.
+ *   R           rows of y, gate and residual.  Rows outside [offsets[0], offsets[E]) of y are
+ *               left as they were.
+ *   Requires 1 <= E <= TGEMM_MAX_EXPERTS, R and x_rows >= 1.
+ *   workspace: tgemm_grouped_workspace_size(op, R, E, N, K) bytes, 256-byte aligned.
+ */
+#define TGEMM_MAX_EXPERTS 1024
+int tgemm_q2_grouped(const uint16_t* x, int x_rows, const uint8_t* wq, const uint16_t* d, const int32_t* offsets,
+                     const int32_t* rows, const tgemm_epilogue* ep, void* y, int R, int E, int N, int K,
+                     int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+int tgemm_q4_grouped(const uint16_t* x, int x_rows, const uint8_t* wq, const uint16_t* sz, const int32_t* offsets,
+                     const int32_t* rows, const tgemm_epilogue* ep, void* y, int R, int E, int N, int K,
+                     int out_dtype, void* workspace, size_t ws_bytes, void* stream);
+size_t tgemm_grouped_workspace_size(int op, int R, int E, int N, int K);
+
+/*
+ * tgemm_expert_sort -- the plan of a grouped matmul: the T * k (token, choice) pairs sorted by
+ * expert, pairs of one expert in their order.
+ *   ids      int32 [T][k], the experts that each token goes to.  An id outside [0, E) leaves
+ *            its pair out.
+ *   offsets  int32 [E + 1] out: expert e's sorted rows are [offsets[e], offsets[e + 1])
+ *   rows     int32 [T * k] out: the token of each sorted row; -1 behind the last
+ *   pos      int32 [T][k] out: the sorted row of each pair; -1 for a pair left out
+ *   workspace of tgemm_expert_sort_workspace_size(T, k, E) bytes (256-byte aligned; 0: none).
+ *   All pointers 4-byte aligned; the outputs must not overlap each other or ids.
+ *   T * k of at most 2^26 (TGEMM_ETOOLARGE beyond).
+ */
+int tgemm_expert_sort(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* rows, int32_t* pos,
+                      void* workspace, size_t ws_bytes, void* stream);
+size_t tgemm_expert_sort_workspace_size(int T, int k, int E);
+
+/*
+ * tgemm_expert_combine -- each token's weighted sum of its experts' outputs:
+ *   y[t] = residual[t] + sum_j weights[t][j] * h[pos[t][j]]
+ *   h        [R][N] f32 or bf16 by h_dtype (16-byte aligned)
+ *   pos      int32 [T][k] (4-byte aligned); an index outside [0, R) leaves its pair out
+ *   weights  f32 [T][k] (4-byte aligned)
+ *   residual [T][N], f32 or bf16 by residual_dtype (16-byte aligned), or null
+ *   y        [T][N] by out_dtype (16-byte aligned); may be the residual (of y's type), no
+ *            other overlap.
+ *   The sum is f32, in the order of j: the same inputs give the same bits.
+ */
+int tgemm_expert_combine(const void* h, int h_dtype, const int32_t* pos, const float* weights, const void* residual,
+                         int residual_dtype, void* y, int T, int k, int N, int R, int out_dtype, void* stream);
+
 /* tgemm_strerror -- a static string describing a TGEMM_* status code. */
 const char* tgemm_strerror(int status);
 
