@@ -49,12 +49,12 @@ int et_pick_nt(int M, int tiles_n, int sms) {
   return best;
 }
 
-template <int FMT, bool SPLIT>
+template <int FMT, bool SPLIT, bool SUMS>
 int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(ep_tc_kernel<FMT, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    err = cudaFuncSetAttribute(ep_tc_kernel<FMT, SPLIT, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                EtFmt<FMT>::kSmemBytes);
   });
   if (err != cudaSuccess) return TGEMM_ECUDA;
@@ -72,7 +72,7 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
                           FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
     return e;
   return launch(FMT == 0 ? TGEMM_KIND_TC_Q2 : TGEMM_KIND_TC_Q4, st, [&] {
-    return pdl_launch(ep_tc_kernel<FMT, SPLIT>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm_x128, tm_x16,
+    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm_x128, tm_x16,
                       tm_w, p);
   });
 }
@@ -160,8 +160,8 @@ int run_ep(const EpCall& c) {
   tiles = std::min<int64_t>(tiles, c.R) * p.tiles_n;
   if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sms));
-  if (c.fmt == 0) return launch_ep_tc<0, false>(c, p, grid, st);
-  return split ? launch_ep_tc<1, true>(c, p, grid, st) : launch_ep_tc<1, false>(c, p, grid, st);
+  if (c.fmt == 0) return out_f32 ? launch_ep_tc<0, false, true>(c, p, grid, st) : launch_ep_tc<0, false, false>(c, p, grid, st);
+  return split ? launch_ep_tc<1, true, true>(c, p, grid, st) : launch_ep_tc<1, false, false>(c, p, grid, st);
 }
 
 // ---- expert sort and combine ---------------------------------------------------------------

@@ -28,8 +28,6 @@ constexpr int kEtXBytes = 2 * kEtXBox;
 constexpr int kEtMaxExperts = 1024;
 constexpr int kEtBoxPitch = kEtRows + 4;        // floats per token row of an output box
 constexpr int kEtBoxFloats = 16 * kEtBoxPitch;
-constexpr int kEtACol0 = 2 * kEtTok;            // two accumulators, then the A stages
-static_assert(kEtACol0 + kEtStages * 64 <= 512, "TMEM budget");
 
 template <int FMT>
 struct EtFmt {
@@ -154,13 +152,22 @@ __device__ __forceinline__ void q4_word_split(uint32_t w, float s, float z, uint
 
 // SPLIT (4-bit weights, f32 y): every 128-k stage runs twice, with the weights' high and low
 // f16 parts, since f16 weights alone are 2^-12 relative off.
-template <int FMT, bool SPLIT>
+//
+// SUMS (f32 y): the tensor core adds each K = 16 step to the f32 accumulator with truncation,
+// 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every kSeg units the
+// accumulator goes into a running sum in tensor memory, rounded to nearest.  That leaves room
+// for two A stages instead of four.
+constexpr int kEtSumCol0 = 2 * kEtTok;
+template <int FMT, bool SPLIT, bool SUMS>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ CUtensorMap tm_x128,
                  const __grid_constant__ CUtensorMap tm_x16,
                  const __grid_constant__ CUtensorMap tm_w, const EtParams p) {
   using F = EtFmt<FMT>;
-  constexpr int kParts = SPLIT ? 2 : 1;
+  constexpr int kA = SUMS ? 2 : 4;                                 // A stages
+  constexpr int kACol0 = SUMS ? kEtSumCol0 + kEtTok : 2 * kEtTok;  // their columns
+  static_assert(kACol0 + 64 * kA <= 512, "TMEM budget");
+  constexpr int kSeg = 4;
   extern __shared__ uint8_t et_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(et_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -262,37 +269,44 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
-      uint32_t it = 0, tc = 0;
+      uint32_t it = 0, sc = 0;  // units, accumulator segments
       bool ok = true;
       int e = 0;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x, ++tc) {
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, static_cast<uint32_t>((tl.mt + 15) & ~15));
-        const uint32_t a = tc & 1u;
-        if (!mbar_wait(accempty_bar(a), ((tc >> 1) & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + a * kEtTok;
-        for (int u = 0; u < ksteps; ++u, ++it) {
-          const uint32_t s = it % kEtStages, ph = (it / kEtStages) & 1u;
-          if (!mbar_wait(full_bar(s), ph, abort_flag)) {
+        for (int u0 = 0; ok && u0 < ksteps; u0 += kSeg, ++sc) {
+          const int u1 = SUMS ? min(u0 + kSeg, ksteps) : ksteps;
+          const uint32_t a = sc & 1u;
+          if (!mbar_wait(accempty_bar(a), ((sc >> 1) & 1u) ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_tmem = tmem_base + kEtACol0 + s * 64;
-          const uint64_t b0 = smem_desc_sw128(sbase + F::kXOff + s * kEtXBytes);
-          const uint64_t b1 = smem_desc_sw128(sbase + F::kXOff + s * kEtXBytes + kEtXBox);
+          const uint32_t d_tmem = tmem_base + a * kEtTok;
+          for (int u = u0; u < u1; ++u, ++it) {
+            const uint32_t s = it % kEtStages, ph = (it / kEtStages) & 1u;
+            if (!mbar_wait(full_bar(s), ph, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_tmem = tmem_base + kACol0 + (it % kA) * 64;
+            const uint64_t b0 = smem_desc_sw128(sbase + F::kXOff + s * kEtXBytes);
+            const uint64_t b1 = smem_desc_sw128(sbase + F::kXOff + s * kEtXBytes + kEtXBox);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
-                       (u > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(empty_bar(s));
+            for (int kk = 0; kk < 8; ++kk)
+              mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
+                         (u > u0 || kk > 0) ? 1u : 0u);
+            mma_commit(empty_bar(s));
+          }
+          if (!ok) break;
+          mma_commit(accfull_bar(a));
+          if (!SUMS) {
+            ++sc;
+            break;
+          }
         }
-        if (!ok) break;
-        mma_commit(accfull_bar(a));
       }
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0u);
@@ -303,7 +317,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const int grp = (warp - kEtDeqWarp0) >> 2;     // which stages: it % kEtGroups == grp
     const int rt = 32 * q + lane;                  // weight row within the tile
     const int nscale = FMT == 0 ? p.K / 128 : p.K / 64;
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kEtACol0;
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kACol0;
     const uint32_t w_mine = sbase + F::kWOff + rt * F::kWqRowBytes;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
     const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
@@ -354,7 +368,6 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(wempty_bar(w));
-        const uint32_t s = i % kEtStages, ph = (i / kEtStages) & 1u;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t o[32];
@@ -379,19 +392,21 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             }
           }
           if (h == 0) {
-            if (!mbar_wait_warp(empty_bar(s), ph ^ 1u, abort_flag)) {
+            // the A stage is free once unit i - kA, which had it before, is multiplied
+            const uint32_t j = i - kA;
+            if (i >= kA && !mbar_wait_warp(empty_bar(j % kEtStages), (j / kEtStages) & 1u, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
           }
-          tmem_st_32x32b_x32(a_lane + s * 64 + 32 * h, o);
+          tmem_st_32x32b_x32(a_lane + (i % kA) * 64 + 32 * h, o);
         }
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar(s));
+        if (lane == 0) mbar_arrive(full_bar(i % kEtStages));
       }
     }
   } else if (warp < kEtWProdWarp) {
@@ -401,30 +416,86 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const EpArgs& a = p.ep;
     const bool vec = (p.N & 3) == 0;             // 4 outputs at a time stay aligned
     float* boxes = reinterpret_cast<float*>(smem + F::kBoxOff) + 2 * set * kEtBoxFloats;
-    uint32_t tc = 0, bc = 0;  // tiles done, boxes filled by this set
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    uint32_t sc = 0, bc = 0;  // segments done, boxes filled by this set
     bool ok = true;
     int e = 0;
-    for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x, ++tc) {
+    auto release = [&](uint32_t ab) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accempty_bar(ab));
+    };
+    for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
       const EtTile tl = et_tile(p, tb, t, e);
-      const uint32_t ab = tc & 1u;
       const int n = tl.n0 + 32 * q + lane;       // this thread's weight row
+      const int n4 = tl.n0 + 4 * lane;           // its 4 rows in the copy-out
       float bias = 0.f;
       if (a.bias && n < p.N) bias = ep_load(a.bias, static_cast<int64_t>(tl.e) * p.N + n, a.bias_f32);
+      uint2 gate_n = make_uint2(0u, 0u);
+      if (vec && a.gate && !a.gate_rows && n4 < p.N) gate_n = *reinterpret_cast<const uint2*>(a.gate + n4);
       const int chunks = (tl.mt + 15) >> 4;
-      if (!mbar_wait_warp(accfull_bar(ab), (tc >> 1) & 1u, abort_flag)) {
+      // running sum += a segment, in f32 rounded to nearest
+      for (int u = kSeg; SUMS && ok && u < ksteps; u += kSeg, ++sc) {
+        const uint32_t ab = sc & 1u;
+        if (!mbar_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int cc = set; cc < chunks; cc += 2) {
+          uint32_t v[16], w[16];
+          tmem_ld_32x32b_x16(t_lane + ab * kEtTok + 16 * cc, v);
+          if (u > kSeg) tmem_ld_32x32b_x16(t_lane + kEtSumCol0 + 16 * cc, w);
+          tmem_wait_ld();
+          if (u > kSeg) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+          }
+          tmem_st_32x32b_x16(t_lane + kEtSumCol0 + 16 * cc, v);
+        }
+        tmem_wait_st();
+        release(ab);
+      }
+      if (!ok) break;
+      const uint32_t ab = sc & 1u;
+      if (!mbar_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag)) {
         ok = false;
         break;
       }
+      ++sc;
       tc_fence_after();
-      const uint32_t tsrc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + ab * kEtTok;
+      if (set >= chunks) release(ab);
       for (int cc = set; cc < chunks; cc += 2, ++bc) {
+        const int m0 = tl.m0 + 16 * cc + 4 * q;  // this warp's 4 tokens in the copy-out
+        const int mt = min(4, tl.mt - 16 * cc - 4 * q);
+        const int64_t i0 = static_cast<int64_t>(m0) * p.N + n4;
+        EpOperands4 in[4];
+        if (vec && n4 < p.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < mt) ep_fetch4(a, i0 + static_cast<int64_t>(i) * p.N, in[i]);
+        }
         uint32_t v[16];
-        tmem_ld_32x32b_x16(tsrc + 16 * cc, v);
-        tmem_wait_ld();
+        tmem_ld_32x32b_x16(t_lane + ab * kEtTok + 16 * cc, v);
+        float f[16];
+        if (SUMS && ksteps > kSeg) {
+          uint32_t w[16];
+          tmem_ld_32x32b_x16(t_lane + kEtSumCol0 + 16 * cc, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]) + __uint_as_float(v[i]);
+        } else {
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+        }
+        if (cc + 2 >= chunks) release(ab);  // the accumulator is read out
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] += bias;
+        ep_act_all(f, a.act);
         float* box = boxes + (bc & 1u) * kEtBoxFloats;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          box[i * kEtBoxPitch + 32 * q + lane] = ep_act(__uint_as_float(v[i]) + bias, a.act);
+        for (int i = 0; i < 16; ++i) box[i * kEtBoxPitch + 32 * q + lane] = f[i];
         __syncwarp();
         if (lane == 0) mbar_arrive(box_bar(set, bc & 1u));
         if (!mbar_wait_warp(box_bar(set, bc & 1u), (bc >> 1) & 1u, abort_flag)) {
@@ -434,22 +505,25 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         // this warp's 4 tokens of the chunk, 128 weight rows each.  With two boxes one
         // meeting per chunk is enough: a box is written again only after every warp has
         // come to the next meeting, and so has read this one.
-        const int mt = min(4, tl.mt - 16 * cc - 4 * q);
-        for (int i = 0; i < mt; ++i) {
-          const int64_t m = tl.m0 + 16 * cc + 4 * q + i;
-          const float* src = box + (4 * q + i) * kEtBoxPitch;
+        if (vec) {
+          if (n4 < p.N) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int nn = tl.n0 + 32 * j + lane;
-            if (nn < p.N) ep_store1(a, m, nn, p.N, src[32 * j + lane]);
+            for (int i = 0; i < 4; ++i)
+              if (i < mt)
+                ep_store4(a, i0 + static_cast<int64_t>(i) * p.N, in[i], gate_n,
+                          *reinterpret_cast<const float4*>(box + (4 * q + i) * kEtBoxPitch + 4 * lane));
+          }
+        } else {
+          for (int i = 0; i < mt; ++i) {
+            const float* src = box + (4 * q + i) * kEtBoxPitch;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int nn = tl.n0 + 32 * j + lane;
+              if (nn < p.N) ep_store1(a, m0 + i, nn, p.N, src[32 * j + lane]);
+            }
           }
         }
       }
-      (void)vec;
-      // the accumulator is read out
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(accempty_bar(ab));
     }
   } else {
     // ------------------------------------------------------------ packed-weight producer
@@ -484,7 +558,6 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
-  (void)kParts;
 }
 
 // The f16 copy of the activations in the dequantizers' k order, row by row: row r of the copy

@@ -17,14 +17,36 @@ struct EpArgs {
   int bias_f32, gate_rows, residual_f32, out_f32, act;
 };
 
-__device__ __forceinline__ float ep_act(float v, int act) {
-  switch (act) {
-    case kActSilu: return v / (1.f + expf(-v));
-    case kActGelu: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case kActGeluTanh: return 0.5f * v * (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * v * v, v, v)));
-    case kActRelu: return v < 0.f ? 0.f : v;  // keeps a NaN
-    default: return v;
+// v / (1 + exp(-t)).  The quotient is within 2 f32 steps; a denominator past 2^126 gives 0,
+// as v * 2^-126 would round to for any v of use.
+__device__ __forceinline__ float ep_logistic(float v, float t) { return __fdividef(v, 1.f + expf(-t)); }
+
+template <int ACT>
+__device__ __forceinline__ float ep_act(float v) {
+  if (ACT == kActSilu) return ep_logistic(v, v);
+  if (ACT == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+  // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)),  2 u = 2 sqrt(2 / pi) (v + 0.044715 v^3)
+  if (ACT == kActGeluTanh) return ep_logistic(v, 1.5957691216057308f * fmaf(0.044715f * v * v, v, v));
+  if (ACT == kActRelu) return v < 0.f ? 0.f : v;  // keeps a NaN
+  return v;
+}
+
+// f(v) for each of n values, the activation chosen once.
+template <int n>
+__device__ __forceinline__ void ep_act_all(float (&v)[n], int act) {
+#define TGEMM_EP_ALL(A)                            \
+  case A: {                                        \
+    _Pragma("unroll") for (int i = 0; i < n; ++i) v[i] = ep_act<A>(v[i]); \
+    break;                                         \
   }
+  switch (act) {
+    TGEMM_EP_ALL(kActSilu)
+    TGEMM_EP_ALL(kActGelu)
+    TGEMM_EP_ALL(kActGeluTanh)
+    TGEMM_EP_ALL(kActRelu)
+    default: break;
+  }
+#undef TGEMM_EP_ALL
 }
 
 __device__ __forceinline__ float ep_load(const void* p, int64_t i, int f32) {
@@ -44,6 +66,53 @@ __device__ __forceinline__ void ep_store1(const EpArgs& a, int64_t m, int n, int
     static_cast<float*>(a.y)[i] = v;
   else
     static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
+}
+
+// The same for 4 consecutive outputs (N a multiple of 4), in two steps: ep_fetch4 issues the
+// loads of gate and residual, ep_store4 uses them.
+struct EpOperands4 {
+  uint2 gate;
+  uint4 res;  // 4 f32, or 4 bf16 in x, y
+};
+__device__ __forceinline__ void ep_fetch4(const EpArgs& a, int64_t i, EpOperands4& o) {
+  if (a.gate && a.gate_rows) o.gate = *reinterpret_cast<const uint2*>(a.gate + i);
+  if (a.residual) {
+    if (a.residual_f32) {
+      o.res = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + i);
+    } else {
+      const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + i);
+      o.res.x = r.x;
+      o.res.y = r.y;
+    }
+  }
+}
+// gate_n: gate[n .. n + 3] when one row of it serves every token
+__device__ __forceinline__ void ep_store4(const EpArgs& a, int64_t i, const EpOperands4& o, uint2 gate_n, float4 v) {
+  if (a.gate) {
+    const uint2 g = a.gate_rows ? o.gate : gate_n;
+    v.x *= __uint_as_float(g.x << 16);
+    v.y *= __uint_as_float(g.x & 0xFFFF0000u);
+    v.z *= __uint_as_float(g.y << 16);
+    v.w *= __uint_as_float(g.y & 0xFFFF0000u);
+  }
+  if (a.residual) {
+    if (a.residual_f32) {
+      v.x += __uint_as_float(o.res.x);
+      v.y += __uint_as_float(o.res.y);
+      v.z += __uint_as_float(o.res.z);
+      v.w += __uint_as_float(o.res.w);
+    } else {
+      v.x += __uint_as_float(o.res.x << 16);
+      v.y += __uint_as_float(o.res.x & 0xFFFF0000u);
+      v.z += __uint_as_float(o.res.y << 16);
+      v.w += __uint_as_float(o.res.y & 0xFFFF0000u);
+    }
+  }
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + i) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + i) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 }  // namespace tgemm
