@@ -77,6 +77,72 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   });
 }
 
+// Small path: the number of warps that share an item, by the rounds of items the GPU's warps
+// need.  An item's end (sums through shared memory, epilogue) costs about two units.
+int es_pick_ks(int64_t items, int U, int warps) {
+  int best = 1;
+  int64_t best_cost = INT64_MAX;
+  for (int ks = 1; ks <= kEsWarps && (ks == 1 || ks <= U); ks *= 2) {
+    const int64_t cost = (items * ks + warps - 1) / warps * ((U + ks - 1) / ks + 2);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = ks;
+    }
+  }
+  return best;
+}
+
+template <int FMT, int T, int RH>
+int launch_ep_small(EsParams p, int64_t tiles, int sms, cudaStream_t st) {
+  p.tiles_n = (p.N + 16 * RH - 1) / (16 * RH);
+  const int64_t items = tiles * p.tiles_n;
+  if (items > INT32_MAX / 2) return TGEMM_ETOOLARGE;
+  p.KS = es_pick_ks(items, p.U, 2 * sms * kEsWarps);
+  const int groups = kEsWarps / p.KS;
+  const int grid = static_cast<int>(std::min<int64_t>((items + groups - 1) / groups, 2 * sms));
+  const size_t smem = es_smem_bytes(T, p.offsets != nullptr);
+  return launch(FMT == 0 ? TGEMM_KIND_GEMV_Q2 : TGEMM_KIND_GEMV_Q4, st, [&] {
+    return pdl_launch(ep_small_kernel<FMT, T, RH>, grid, kEsWarps * 32, smem, st, p);
+  });
+}
+
+// The most row chunks of `nt` that R rows in E groups can make.
+int64_t max_chunks(int R, int E, int nt) {
+  return std::min<int64_t>(R, static_cast<int64_t>(R) / nt + std::min(R, E));
+}
+
+int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
+  EsParams p = {};
+  p.N = c.N;
+  p.K = c.K;
+  p.E = c.E;
+  p.R = c.R;
+  p.x_rows = c.x_rows;
+  p.U = (c.K + 127) / 128;
+  p.x = c.x;
+  p.wq = c.wq;
+  p.scales = c.scales;
+  p.offsets = c.offsets;
+  p.rows = c.rows;
+  p.ep = a;
+  const int per = c.offsets ? (c.R + c.E - 1) / c.E : c.R;  // rows of an expert, on average
+  auto go = [&](auto fmt_c) {
+    constexpr int kF = decltype(fmt_c)::value;
+    if (per <= 8) return launch_ep_small<kF, 1, 2>(p, max_chunks(c.R, c.E, 8), sms, st);
+    if (per <= 16) return launch_ep_small<kF, 2, 2>(p, max_chunks(c.R, c.E, 16), sms, st);
+    return launch_ep_small<kF, 4, 1>(p, max_chunks(c.R, c.E, 32), sms, st);
+  };
+  return c.fmt == 0 ? go(std::integral_constant<int, 0>{}) : go(std::integral_constant<int, 1>{});
+}
+
+// Whether the small path serves a call (see ep_small.cuh); tgemm_set_path overrides it.
+bool ep_is_small(int R, int E, bool grouped) {
+  const int p = g_path.load();
+  if (p == TGEMM_PATH_TENSOR) return false;
+  if (p != TGEMM_PATH_AUTO) return true;
+  return grouped ? R <= 16 : R <= 16;
+}
+
 int run_ep(const EpCall& c) {
   const int kblock = c.fmt == 0 ? 128 : 64;
   if (!c.x || !c.wq || !c.scales || !c.y) return TGEMM_EINVAL;
@@ -126,13 +192,15 @@ int run_ep(const EpCall& c) {
       overlaps(c.y, y_bytes, c.offsets, c.offsets ? (static_cast<size_t>(c.E) + 1) * 4 : 0) ||
       overlaps(c.y, y_bytes, c.rows, c.rows ? static_cast<size_t>(c.R) * 4 : 0))
     return TGEMM_EINVAL;
-  const size_t need = ep_x16_bytes(c.R, c.K);
-  if (!c.workspace || c.ws_bytes < need) return TGEMM_EWORKSPACE;
-  if (!aligned(c.workspace, 256)) return TGEMM_EALIGN;
-  if (overlaps(c.y, y_bytes, c.workspace, need)) return TGEMM_EINVAL;
+  const bool small = ep_is_small(c.R, c.E, c.offsets != nullptr);
+  const size_t need = small ? 0 : ep_x16_bytes(c.R, c.K);
+  if (need && (!c.workspace || c.ws_bytes < need)) return TGEMM_EWORKSPACE;
+  if (need && !aligned(c.workspace, 256)) return TGEMM_EALIGN;
+  if (need && overlaps(c.y, y_bytes, c.workspace, need)) return TGEMM_EINVAL;
   DeviceInfo di;
   if (int e = current_device_info(&di)) return e;
   const cudaStream_t st = as_stream(c.stream);
+  if (small) return run_ep_small(c, a, di.sms, st);
 
   uint16_t* x16 = static_cast<uint16_t*>(c.workspace);
   const int pgrid = grid_for(static_cast<int64_t>(c.R) * (c.K / 16), 256, di.sms);
@@ -156,8 +224,7 @@ int run_ep(const EpCall& c) {
   p.scales = c.scales;
   p.ep = a;
   // the most tiles there can be: an expert with rows has at most one partly filled tile
-  int64_t tiles = c.R / p.nt + std::min(c.R, c.E);
-  tiles = std::min<int64_t>(tiles, c.R) * p.tiles_n;
+  const int64_t tiles = max_chunks(c.R, c.E, p.nt) * p.tiles_n;
   if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
   const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sms));
   if (c.fmt == 0) return out_f32 ? launch_ep_tc<0, false, true>(c, p, grid, st) : launch_ep_tc<0, false, false>(c, p, grid, st);

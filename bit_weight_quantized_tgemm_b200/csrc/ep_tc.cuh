@@ -72,9 +72,21 @@ struct EtTable {
 struct EtTile {
   int e, n0, m0, mt;  // expert, first weight row, first token row, tokens
 };
-// Tile t of the walk (t never decreases; e is the walk's position).
+// The expert with token tile tt: the largest e with tp[e] <= tt (and so tt < tp[e + 1]).
+__device__ __forceinline__ int et_find(const int* tp, int E, int tt) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tp[mid] <= tt)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+// Tile t of the walk (e is the walk's position, looked up again once t leaves that expert).
 __device__ __forceinline__ EtTile et_tile(const EtParams& p, const EtTable& tb, int t, int& e) {
-  while (t >= tb.tp[e + 1] * p.tiles_n) ++e;
+  if (t >= tb.tp[e + 1] * p.tiles_n) e = et_find(tb.tp, p.E, t / p.tiles_n);
   const int tt = tb.tp[e + 1] - tb.tp[e];
   const int r = t - tb.tp[e] * p.tiles_n;
   const int tn = r / tt, ti = r - tn * tt;
@@ -88,26 +100,26 @@ __device__ __forceinline__ EtTile et_tile(const EtParams& p, const EtTable& tb, 
 
 // Group offsets come from the device and are not trusted: each is clamped to [previous, R],
 // so that every row range lies inside the caller's buffers.
-__device__ __forceinline__ void et_build_table(const EtParams& p, int* off, int* tp) {
+__device__ __forceinline__ void et_build_table(const int* offsets, int E, int R, int nt, int* off, int* tp) {
   const int lane = threadIdx.x & 31;
-  int run = 0, tiles = 0;
-  if (!p.offsets) {
+  if (!offsets) {
     if (lane == 0) {
       off[0] = 0;
-      off[1] = p.R;
+      off[1] = R;
       tp[0] = 0;
-      tp[1] = (p.R + p.nt - 1) / p.nt;
+      tp[1] = (R + nt - 1) / nt;
     }
     return;
   }
-  run = min(max(__ldg(p.offsets), 0), p.R);
+  int tiles = 0;
+  int run = min(max(__ldg(offsets), 0), R);
   if (lane == 0) {
     off[0] = run;
     tp[0] = 0;
   }
-  for (int e0 = 0; e0 < p.E; e0 += 32) {
+  for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    int v = e < p.E ? min(max(__ldg(p.offsets + e + 1), 0), p.R) : 0;
+    int v = e < E ? min(max(__ldg(offsets + e + 1), 0), R) : 0;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, v, s);
@@ -116,14 +128,14 @@ __device__ __forceinline__ void et_build_table(const EtParams& p, int* off, int*
     v = max(v, run);
     int prev = __shfl_up_sync(0xFFFFFFFFu, v, 1);
     if (lane == 0) prev = run;
-    int c = (v - prev + p.nt - 1) / p.nt;
+    int c = (v - prev + nt - 1) / nt;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, c, s);
       if (lane >= s) c += o;
     }
     c += tiles;
-    if (e < p.E) {
+    if (e < E) {
       off[e + 1] = v;
       tp[e + 1] = c;
     }
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   // With device offsets every role needs them first; a dense call's weights are read early,
   // and only the activation producer and the epilogue wait.
   if (p.offsets || warp == 0 || (warp >= kEtEpiWarp0 && warp < kEtWProdWarp)) pdl_wait();
-  if (warp == kEtWProdWarp) et_build_table(p, tab_off, tab_tp);
+  if (warp == kEtWProdWarp) et_build_table(p.offsets, p.E, p.R, p.nt, tab_off, tab_tp);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
