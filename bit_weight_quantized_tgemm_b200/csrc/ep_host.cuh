@@ -35,10 +35,10 @@ size_t ep_x16_bytes(int R, int K) { return round_up(static_cast<size_t>(R) * K *
 // Tokens per tile of a dense call: the candidate whose fullest CTA has the least to do.  A
 // 128-k stage costs 4 cycles per token on the tensor core and no less than the dequantizers
 // need for its 128 x 128 weights.
-int et_pick_nt(int M, int tiles_n, int sms) {
-  int best = kEtTok;
+int et_pick_nt(int M, int tiles_n, int most, int sms) {
+  int best = most;
   int64_t best_cost = INT64_MAX;
-  for (int nt = 16; nt <= kEtTok; nt += 16) {
+  for (int nt = 16; nt <= most; nt += 16) {
     const int64_t tiles = static_cast<int64_t>((M + nt - 1) / nt) * tiles_n;
     const int64_t cost = (tiles + sms - 1) / sms * std::max(4 * nt, 350);
     if (cost <= best_cost) {
@@ -58,22 +58,30 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
                                EtFmt<FMT>::kSmemBytes);
   });
   if (err != cudaSuccess) return TGEMM_ECUDA;
-  CUtensorMap tm_x128, tm_x16, tm_w;
-  const uint64_t rows = static_cast<uint64_t>(c.R);
-  if (int e = make_map_2d(&tm_x128, c.workspace, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.K, rows, 64, kEtTok,
-                          CU_TENSOR_MAP_SWIZZLE_128B))
-    return e;
-  if (int e = make_map_2d(&tm_x16, c.workspace, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.K, rows, 64, 16,
-                          CU_TENSOR_MAP_SWIZZLE_128B))
-    return e;
+  EtMaps tm;
+  for (int i = 0; i < 4; ++i) {
+    if (i > 0 && (8 << i) >= p.nt) {  // no tile is that large
+      tm.x[i] = tm.x[0];
+      continue;
+    }
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.K) * 2, 128};
+    const cuuint32_t box[3] = {64, 16u << i, 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    if (int e = encoder(&enc)) return e;
+    if (enc(&tm.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, c.workspace, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return TGEMM_ECUDA;
+  }
   const uint64_t row_bytes = static_cast<uint64_t>(c.K) / (FMT == 0 ? 4 : 2);
-  if (int e = make_map_2d(&tm_w, c.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row_bytes,
+  if (int e = make_map_2d(&tm.w, c.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row_bytes,
                           static_cast<uint64_t>(c.E) * c.N, EtFmt<FMT>::kWqRowBytes, kEtRows,
                           FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
     return e;
   return launch(FMT == 0 ? TGEMM_KIND_TC_Q2 : TGEMM_KIND_TC_Q4, st, [&] {
-    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm_x128, tm_x16,
-                      tm_w, p);
+    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm, p);
   });
 }
 
@@ -218,7 +226,8 @@ int run_ep(const EpCall& c) {
   p.E = c.E;
   p.R = c.R;
   p.tiles_n = (c.N + kEtRows - 1) / kEtRows;
-  p.nt = c.offsets ? kEtTok : et_pick_nt(c.R, p.tiles_n, di.sms);
+  const int most = out_f32 ? kEtSumTok : kEtTok;  // tokens of a tile
+  p.nt = c.offsets ? most : et_pick_nt(c.R, p.tiles_n, most, di.sms);
   p.ksteps = (c.K + kEtBK - 1) / kEtBK * (split ? 2 : 1);
   p.offsets = c.offsets;
   p.scales = c.scales;

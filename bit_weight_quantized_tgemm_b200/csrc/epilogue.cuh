@@ -68,51 +68,4 @@ __device__ __forceinline__ void ep_store1(const EpArgs& a, int64_t m, int n, int
     static_cast<__nv_bfloat16*>(a.y)[i] = __float2bfloat16_rn(v);
 }
 
-// The same for 4 consecutive outputs (N a multiple of 4), in two steps: ep_fetch4 issues the
-// loads of gate and residual, ep_store4 uses them.
-struct EpOperands4 {
-  uint2 gate;
-  uint4 res;  // 4 f32, or 4 bf16 in x, y
-};
-__device__ __forceinline__ void ep_fetch4(const EpArgs& a, int64_t i, EpOperands4& o) {
-  if (a.gate && a.gate_rows) o.gate = *reinterpret_cast<const uint2*>(a.gate + i);
-  if (a.residual) {
-    if (a.residual_f32) {
-      o.res = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + i);
-    } else {
-      const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + i);
-      o.res.x = r.x;
-      o.res.y = r.y;
-    }
-  }
-}
-// gate_n: gate[n .. n + 3] when one row of it serves every token
-__device__ __forceinline__ void ep_store4(const EpArgs& a, int64_t i, const EpOperands4& o, uint2 gate_n, float4 v) {
-  if (a.gate) {
-    const uint2 g = a.gate_rows ? o.gate : gate_n;
-    v.x *= __uint_as_float(g.x << 16);
-    v.y *= __uint_as_float(g.x & 0xFFFF0000u);
-    v.z *= __uint_as_float(g.y << 16);
-    v.w *= __uint_as_float(g.y & 0xFFFF0000u);
-  }
-  if (a.residual) {
-    if (a.residual_f32) {
-      v.x += __uint_as_float(o.res.x);
-      v.y += __uint_as_float(o.res.y);
-      v.z += __uint_as_float(o.res.z);
-      v.w += __uint_as_float(o.res.w);
-    } else {
-      v.x += __uint_as_float(o.res.x << 16);
-      v.y += __uint_as_float(o.res.x & 0xFFFF0000u);
-      v.z += __uint_as_float(o.res.y << 16);
-      v.w += __uint_as_float(o.res.y & 0xFFFF0000u);
-    }
-  }
-  if (a.out_f32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + i) = v;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + i) =
-        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-
 }  // namespace tgemm
