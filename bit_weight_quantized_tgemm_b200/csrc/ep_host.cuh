@@ -29,8 +29,8 @@ struct EpCall {
 
 bool dtype_ok(int dt) { return dt == TGEMM_OUT_F32 || dt == TGEMM_OUT_BF16; }
 
-// Bytes of the f16 copy of the activations (tensor-core path).
-size_t ep_x16_bytes(int R, int K) { return round_up(static_cast<size_t>(R) * K * 2, 256); }
+// Workspace of the tensor-core path: the f16 copy of the activations.
+size_t ep_ws_bytes(int R, int K) { return round_up(static_cast<size_t>(R) * K * 2, 256); }
 
 // Tokens per tile of a dense call: the candidate whose fullest CTA has the least to do.  A
 // 128-k stage costs 4 cycles per token on the tensor core and no less than the dequantizers
@@ -59,17 +59,14 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   });
   if (err != cudaSuccess) return TGEMM_ECUDA;
   EtMaps tm;
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  if (int e = encoder(&enc)) return e;
   for (int i = 0; i < 4; ++i) {
-    if (i > 0 && (8 << i) >= p.nt) {  // no tile is that large
-      tm.x[i] = tm.x[0];
-      continue;
-    }
+    if (i > 0 && (8 << i) >= p.nt) break;  // no tile is that large
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.K) * 2, 128};
     const cuuint32_t box[3] = {64, 16u << i, 2};
     const cuuint32_t estr[3] = {1, 1, 1};
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    if (int e = encoder(&enc)) return e;
     if (enc(&tm.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, c.workspace, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -201,7 +198,7 @@ int run_ep(const EpCall& c) {
       overlaps(c.y, y_bytes, c.rows, c.rows ? static_cast<size_t>(c.R) * 4 : 0))
     return TGEMM_EINVAL;
   const bool small = ep_is_small(c.R, c.E, c.offsets != nullptr);
-  const size_t need = small ? 0 : ep_x16_bytes(c.R, c.K);
+  const size_t need = small ? 0 : ep_ws_bytes(c.R, c.K);
   if (need && (!c.workspace || c.ws_bytes < need)) return TGEMM_EWORKSPACE;
   if (need && !aligned(c.workspace, 256)) return TGEMM_EALIGN;
   if (need && overlaps(c.y, y_bytes, c.workspace, need)) return TGEMM_EINVAL;
@@ -229,6 +226,7 @@ int run_ep(const EpCall& c) {
   const int most = out_f32 ? kEtSumTok : kEtTok;  // tokens of a tile
   p.nt = c.offsets ? most : et_pick_nt(c.R, p.tiles_n, most, di.sms);
   p.ksteps = (c.K + kEtBK - 1) / kEtBK * (split ? 2 : 1);
+  p.nblocks = c.K / (c.fmt == 0 ? 128 : 64);
   p.offsets = c.offsets;
   p.scales = c.scales;
   p.ep = a;

@@ -20,15 +20,24 @@ constexpr int kEtSumTok = 80;                   // most tokens of a tile with ru
 constexpr int kEtBK = 128;
 constexpr int kEtGroups = 3;                    // dequant groups of 4 warps, stages in turn
 constexpr int kEtWProdWarp = 2;
-constexpr int kEtDeqWarp0 = 3;
+constexpr int kEtScaleWarp = 3;
+constexpr int kEtDeqWarp0 = 4;
 constexpr int kEtEpiWarp0 = kEtDeqWarp0 + 4 * kEtGroups;
 constexpr int kEtThreads = (kEtEpiWarp0 + 8) * 32;
 constexpr int kEtXRing = 4 * kEtTok * 256;      // activation ring: 4 slots of 128 tokens or 8 of 64
 constexpr int kEtXSlots = 8;
-constexpr int kEtA = 4;                         // A stages in tensor memory
-constexpr int kEtACol0 = 256;                   // their columns, behind the accumulators
+constexpr int kEtChunk = 16;                    // scale blocks of a chunk
+constexpr int kEtScBufs = 3;                    // chunks of scales in shared memory
 constexpr int kEtMaxExperts = 1024;
-static_assert(3 * kEtSumTok <= kEtACol0 && 2 * kEtTok <= kEtACol0 && kEtACol0 + 64 * kEtA <= 512, "TMEM budget");
+// Tensor memory: two accumulators, the running sum if there is one, and from column `a0` the
+// A stages (64 columns each).
+struct EtTmem {
+  int acc, a0, na;  // columns of an accumulator, first A column, A stages
+};
+__host__ __device__ constexpr EtTmem et_tmem(bool sums, int nt) {
+  return sums ? EtTmem{kEtSumTok, 256, 4} : nt <= 64 ? EtTmem{64, 128, 6} : EtTmem{128, 256, 4};
+}
+static_assert(3 * kEtSumTok <= 256, "two accumulators and the running sum");
 
 template <int FMT>
 struct EtFmt {
@@ -37,9 +46,15 @@ struct EtFmt {
   static constexpr int kWBytes = kEtRows * kWqRowBytes;
   static constexpr int kXOff = 0;
   static constexpr int kWOff = kEtXRing;
-  static constexpr int kTabOff = kWOff + kWStages * kWBytes;
+  // A chunk's scales as 32-bit words [word][row] (Q2: two blocks' d, 4-bit: a block's (s, z)):
+  // the pitch keeps the scale warp's writes and the dequantizers' reads free of bank conflicts.
+  static constexpr int kScWords = FMT == 0 ? kEtChunk / 2 : kEtChunk;
+  static constexpr int kScPitch = 4 * kEtRows + (FMT == 0 ? 16 : 8);
+  static constexpr int kScBytes = kScWords * kScPitch;
+  static constexpr int kScOff = kWOff + kWStages * kWBytes;
+  static constexpr int kTabOff = kScOff + kEtScBufs * kScBytes;
   static constexpr int kBarOff = kTabOff + 2 * (kEtMaxExperts + 2) * 4;
-  static constexpr int kNumBars = 2 * kEtXSlots + 2 * kWStages + 4 + 1;
+  static constexpr int kNumBars = 2 * kEtXSlots + 2 * kWStages + 4 + 1 + 2 * kEtScBufs;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -49,7 +64,8 @@ struct EtParams {
   int N, K, E, R;
   int nt;                 // tokens per tile, a multiple of 16
   int tiles_n;            // ceil(N / 128)
-  int ksteps;             // units per tile: ceil(K / 128), twice that with the low parts
+  int ksteps;             // main units per tile: ceil(K / 128), twice that with the low parts
+  int nblocks;            // scale blocks of a row: K / 128 or K / 64
   const int* offsets;     // [E + 1] row ranges, or null: one expert, rows [0, R)
   const uint16_t* scales;
   EpArgs ep;
@@ -80,34 +96,36 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait with a suspend hint: the waiting warp sleeps in the barrier unit instead of
-// polling, and leaves its issue slots to the dequantizers.  Bounded as mbar_wait is.
-__device__ __forceinline__ bool mbar_try_sleep(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool et_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  if (mbar_try_sleep(bar, parity)) return true;
+// Wait for a phase.  The common case is one try_wait (39 cycles); a warp that has to wait
+// sleeps in the barrier unit and leaves its issue slots to others.  Bounded: after
+// kWaitLimitNs it records a timeout and raises the CTA's abort flag, and every later wait of
+// the CTA returns at once, so that the kernel runs out (with the device error word set).
+__device__ __noinline__ void et_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
-    if (mbar_try_sleep(bar, parity)) return true;
-    if (*abort_flag) return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok || *abort_flag) return;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1u;
       atomicOr(&g_device_error, kDevErrTimeout);
-      return false;
+      return;
     }
   }
 }
-__device__ __forceinline__ bool et_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  return __all_sync(0xFFFFFFFFu, et_wait(bar, parity, abort_flag));
+__device__ __forceinline__ void et_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  if (!mbar_try_wait(bar, parity)) et_wait_slow(bar, parity, abort_flag);
+}
+// By a whole warp, which goes on together.
+__device__ __forceinline__ void et_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  et_wait(bar, parity, abort_flag);
+  __syncwarp();
 }
 
 // Row ranges and token-tile counts of the experts, in shared memory: off[e], off[e + 1]
@@ -220,8 +238,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
   using F = EtFmt<FMT>;
   constexpr int kSeg = 4;
-  constexpr int kAccCols = SUMS ? kEtSumTok : kEtTok;  // columns of an accumulator
-  constexpr int kSumCol0 = 2 * kAccCols;
+  constexpr int kSumCol0 = 2 * kEtSumTok;
+  static_assert(FMT == 1 || !SPLIT, "ternary weights are exact in f16");
+  static_assert(!SPLIT || SUMS, "the low parts are for f32 y");
+  constexpr int kCU = (FMT == 0 ? 16 : 8) * (SPLIT ? 2 : 1);  // main units of a chunk
   extern __shared__ uint8_t et_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(et_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -231,9 +251,12 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kEtXSlots + s); };
   auto wfull_bar = [&](uint32_t w) { return bar0 + 8u * (2 * kEtXSlots + w); };
   auto wempty_bar = [&](uint32_t w) { return bar0 + 8u * (2 * kEtXSlots + F::kWStages + w); };
-  auto accfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kEtXSlots + 2 * F::kWStages + a); };
-  auto accempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kEtXSlots + 2 * F::kWStages + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * kEtXSlots + 2 * F::kWStages + 4);
+  constexpr uint32_t kBar1 = 2 * kEtXSlots + 2 * F::kWStages;
+  auto accfull_bar = [&](uint32_t a) { return bar0 + 8u * (kBar1 + a); };
+  auto accempty_bar = [&](uint32_t a) { return bar0 + 8u * (kBar1 + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (kBar1 + 4);
+  auto sfull_bar = [&](uint32_t b) { return bar0 + 8u * (kBar1 + 5 + b); };
+  auto sempty_bar = [&](uint32_t b) { return bar0 + 8u * (kBar1 + 5 + kEtScBufs + b); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + F::kMiscOff);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + F::kMiscOff + 4);
   int* tab_off = reinterpret_cast<int*>(smem + F::kTabOff);
@@ -257,6 +280,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(accfull_bar(a), 1);
       mbar_init(accempty_bar(a), 8);
+    }
+    for (int b = 0; b < kEtScBufs; ++b) {
+      mbar_init(sfull_bar(b), 32);  // the scale warp's lanes
+      mbar_init(sempty_bar(b), 4 * kEtGroups);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -282,30 +309,26 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const EtTable tb{tab_off, tab_tp};
   const int num_tiles = tab_tp[p.E] * p.tiles_n;
-  const int ksteps = p.ksteps;
+  const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
+  const EtTmem tmm = et_tmem(SUMS, p.nt);
   // activation slots: unit i uses slot i & (nx - 1); deeper when the tiles are small
   const int lx = p.nt <= kEtTok / 2 ? 3 : 2;
   const uint32_t nx = 1u << lx, xslot = kEtXRing >> lx;
 
+  // Every role walks the same stream of units: tile by tile, unit by unit along k.
   if (warp == 0) {
     // ------------------------------------------------------------ activation producer
     if (elect_one()) {
       uint32_t it = 0;
-      bool ok = true;
       int e = 0;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
-        const CUtensorMap* map = &tm.x[box];
-        const uint32_t bytes = 4096u << box;
         for (int u = 0; u < ksteps; ++u, ++it) {
-          const uint32_t s = it & (nx - 1), ph = (it >> lx) & 1u;
-          if (!et_wait(empty_bar(s), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(full_bar(s), bytes);
-          tma_load_3d(sbase + F::kXOff + s * xslot, map, full_bar(s), 0, tl.m0, 2 * (SPLIT ? u >> 1 : u));
+          const uint32_t s = it & (nx - 1);
+          et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
+          mbar_arrive_expect_tx(full_bar(s), 4096u << box);
+          tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * (SPLIT ? u >> 1 : u));
         }
       }
       // every load issued must land before the CTA may exit
@@ -316,42 +339,36 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
       uint32_t it = 0, sc = 0;  // units, accumulator segments
-      bool ok = true;
+      int as = 0;               // A stage
       int e = 0;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
-        const uint32_t idesc = make_idesc_f16(0u, kEtRows, static_cast<uint32_t>((tl.mt + 15) & ~15));
+        const uint32_t ncols = static_cast<uint32_t>((tl.mt + 15) & ~15);
+        const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
         const uint32_t half = 2048u << et_box(tl.mt);  // bytes of a k block's box
-        for (int u0 = 0; ok && u0 < ksteps; ++sc) {
-          const int u1 = SUMS ? min(u0 + kSeg, ksteps) : ksteps;
-          const uint32_t a = sc & 1u;
-          if (!et_wait(accempty_bar(a), ((sc >> 1) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
+        uint32_t d_tmem = 0;
+        for (int u = 0; u < ksteps; ++u, ++it) {
+          const bool first = u == 0 || (SUMS && u % kSeg == 0);  // of an accumulator segment
+          if (first) {
+            if (SUMS && u > 0) mma_commit(accfull_bar(sc++ & 1u));
+            et_wait(accempty_bar(sc & 1u), ((sc >> 1) & 1u) ^ 1u, abort_flag);
+            d_tmem = tmem_base + (sc & 1u) * tmm.acc;
           }
+          const uint32_t s = it & (nx - 1);
+          const uint32_t a_tmem = tmem_base + tmm.a0 + as * 64;
+          if (++as == tmm.na) as = 0;
+          const uint32_t xs = sbase + F::kXOff + s * xslot;
+          const uint64_t b0 = smem_desc_sw128(xs);
+          const uint64_t b1 = smem_desc_sw128(xs + half);
+          et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + a * kAccCols;
-          for (int u = u0; u < u1; ++u, ++it) {
-            const uint32_t s = it & (nx - 1), ph = (it >> lx) & 1u;
-            if (!et_wait(full_bar(s), ph, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a_tmem = tmem_base + kEtACol0 + (it % kEtA) * 64;
-            const uint32_t xs = sbase + F::kXOff + s * xslot;
-            const uint64_t b0 = smem_desc_sw128(xs);
-            const uint64_t b1 = smem_desc_sw128(xs + half);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
-                         (u > u0 || kk > 0) ? 1u : 0u);
-            mma_commit(empty_bar(s));
-          }
-          if (!ok) break;
-          mma_commit(accfull_bar(a));
-          u0 = u1;
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
+                       (kk > 0 || !first) ? 1u : 0u);
+          mma_commit(empty_bar(s));
         }
+        mma_commit(accfull_bar(sc++ & 1u));
       }
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0u);
@@ -360,17 +377,13 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     // ------------------------------------------------------------ packed-weight producer
     if (elect_one()) {
       uint32_t it = 0;
-      bool ok = true;
       int e = 0;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int row = tl.e * p.N + tl.n0;
         for (int u = 0; u < ksteps; ++u, ++it) {
-          const uint32_t w = it % F::kWStages, ph = (it / F::kWStages) & 1u;
-          if (!et_wait(wempty_bar(w), ph ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+          const uint32_t w = it % F::kWStages;
+          et_wait(wempty_bar(w), ((it / F::kWStages) & 1u) ^ 1u, abort_flag);
           mbar_arrive_expect_tx(wfull_bar(w), F::kWBytes);
           tma_load_2d(sbase + F::kWOff + w * F::kWBytes, &tm.w, wfull_bar(w),
                       (SPLIT ? u >> 1 : u) * F::kWqRowBytes, row);
@@ -379,123 +392,151 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       for (uint32_t j = (it > F::kWStages ? it - F::kWStages : 0); j < it; ++j)
         mbar_wait_drain(wfull_bar(j % F::kWStages), (j / F::kWStages) & 1u);
     }
+  } else if (warp == kEtScaleWarp) {
+    // ------------------------------------------------------------ scales -> shared memory
+    // A row's scales of a chunk are 32 (Q2) or 64 neighbouring bytes, so a warp's copy of 32
+    // words touches 4 or 2 lines.  (One thread per weight row reading its own scale each unit
+    // touches 32, 32 cycles of the load unit per warp and unit, which bound the kernel.)
+    // Asynchronous copies, as far ahead as the buffers go.
+    constexpr int kW = F::kScWords, kR = 32 / kW;  // words of a row, rows a copy takes
+    const int wd = lane % kW, rl = lane / kW;
+    // pairs of Q2 scales are words only where the rows start on words
+    const bool words = FMT == 1 || ((p.nblocks & 1) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3) == 0);
+    uint32_t cidx = 0;
+    int e = 0;
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+      const EtTile tl = et_tile(p, tb, t, e);
+      const int rows = min(kEtRows, p.N - tl.n0);
+      const int64_t row0 = static_cast<int64_t>(tl.e) * p.N + tl.n0 + rl;
+      for (int c = 0; c < nchunks; ++c, ++cidx) {
+        const uint32_t b = cidx % kEtScBufs;
+        const int k = c * kEtChunk + wd * (kEtChunk / kW);  // the word's (first) block
+        const uint32_t off = F::kScOff + b * F::kScBytes + wd * F::kScPitch + 4 * rl;
+        et_wait_warp(sempty_bar(b), ((cidx / kEtScBufs) & 1u) ^ 1u, abort_flag);
+        if (words) {
+          // rows past N and blocks past K: zeros, no weight
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(p.scales) + (row0 * p.nblocks + k) / (FMT == 0 ? 2 : 1);
+          const int64_t step = static_cast<int64_t>(kR) * p.nblocks / (FMT == 0 ? 2 : 1);
+#pragma unroll 8
+          for (int r = 0; r < kEtRows; r += kR, src += step) {
+            const bool in = r + rl < rows && k < p.nblocks;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sbase + off + 4 * r),
+                         "l"(in ? static_cast<const void*>(src) : static_cast<const void*>(p.scales)), "r"(in ? 4u : 0u)
+                         : "memory");
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull_bar(b)) : "memory");
+        } else {
+#pragma unroll 8
+          for (int r = 0; r < kEtRows; r += kR) {
+            uint32_t v = 0u;
+            if (r + rl < rows) {
+              const uint16_t* src = p.scales + (row0 + r) * p.nblocks + k;
+              if (k < p.nblocks) v = __ldg(src);
+              if (k + 1 < p.nblocks) v |= static_cast<uint32_t>(__ldg(src + 1)) << 16;
+            }
+            *reinterpret_cast<uint32_t*>(smem + off + 4 * r) = v;
+          }
+          mbar_arrive(sfull_bar(b));
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kEtEpiWarp0) {
     // ------------------------------------------------------------ dequantizers
-    // Group grp takes the units i = grp (mod kEtGroups) of the CTA's stream of units; each of
-    // its threads unpacks one weight row's 128 codes of the unit.
+    // Group grp takes every third unit of the stream; each of its threads unpacks one weight
+    // row's 128 codes of the unit.
     const int q = warp & 3;                        // TMEM lane quarter
     const int grp = (warp - kEtDeqWarp0) >> 2;
     const int rt = 32 * q + lane;                  // weight row within the tile
-    const int nscale = FMT == 0 ? p.K / 128 : p.K / 64;
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kEtACol0;
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + tmm.a0;
     const uint32_t w_mine = sbase + F::kWOff + rt * F::kWqRowBytes;
+    const uint8_t* s_mine = smem + F::kScOff + 4 * rt;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
     const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
-    // The scales are loaded two of the group's units ahead, across tiles: position (lt, lu).
-    // They alternate between two sets of registers, never moved: a move would wait for its load.
-    constexpr int kSc = FMT == 0 ? 1 : 2;
-    int lt = blockIdx.x, lu = grp, le = 0;
-    const uint16_t* lrow = nullptr;
-    auto locate = [&]() {  // the row's scales of tile lt (null: no such tile or row)
-      while (lu >= ksteps) {
-        lu -= ksteps;
-        lt += gridDim.x;
-        lrow = nullptr;
-        if (lt >= num_tiles) return;
-      }
-      if (!lrow && lt < num_tiles) {
-        const EtTile tl = et_tile(p, tb, lt, le);
-        if (tl.n0 + rt < p.N)
-          lrow = p.scales + (static_cast<int64_t>(tl.e) * p.N + tl.n0 + rt) * nscale * (FMT == 0 ? 1 : 2);
-      }
-    };
-    auto load_scales = [&](uint32_t (&sc)[kSc]) {
-      sc[0] = sc[kSc - 1] = 0u;
-      if (lt < num_tiles) {
-        const int ks = SPLIT ? lu >> 1 : lu;
-        if (lrow) {
-          if (FMT == 0) {
-            sc[0] = __ldg(lrow + ks);
-          } else {
-            const uint32_t* sp = reinterpret_cast<const uint32_t*>(lrow) + 2 * ks;
-            sc[0] = __ldg(sp);
-            if (2 * ks + 1 < nscale) sc[kSc - 1] = __ldg(sp + 1);
-          }
-        }
-        lu += kEtGroups;
-        locate();
-      }
-    };
-    locate();
-    uint32_t sa[kSc], sb[kSc];
-    load_scales(sa);
-    load_scales(sb);
     const int my_tiles = num_tiles > static_cast<int>(blockIdx.x)
                              ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
-    const uint32_t units = static_cast<uint32_t>(my_tiles) * ksteps;
-    // one unit; false at the end
-    auto unit = [&](uint32_t i, uint32_t (&sn)[kSc]) -> bool {
-      if (i >= units) return false;
-      uint32_t sc[kSc];
-#pragma unroll
-      for (int j = 0; j < kSc; ++j) sc[j] = sn[j];
-      load_scales(sn);
-      const uint32_t w = i % F::kWStages, wph = (i / F::kWStages) & 1u;
-      if (!et_wait_warp(wfull_bar(w), wph, abort_flag)) return false;
-      constexpr int kWords = F::kWqRowBytes / 4;
-      uint32_t cw[kWords];
-#pragma unroll
-      for (int c = 0; c < kWords / 4; ++c) {
-        const uint4 v = ld_shared_v4(w_mine + w * F::kWBytes + ((c ^ swz) << 4));
-        cw[4 * c] = v.x;
-        cw[4 * c + 1] = v.y;
-        cw[4 * c + 2] = v.z;
-        cw[4 * c + 3] = v.w;
-      }
-      // the slot is refilled by TMA (the async proxy) once the group has released it
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(wempty_bar(w));
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {  // 32 codes each
-        uint32_t o[16];
-        if (FMT == 0) {
-          const uint32_t d2 = sc[0] | (sc[0] << 16);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) q2_word_to_f16(cw[2 * h + j], d2, o + 8 * j);
-        } else if (!SPLIT) {
-          const uint32_t s1 = sc[(h >> 1) % kSc];
-          const uint32_t s2 = (s1 & 0xFFFFu) | (s1 << 16);
-          const uint32_t z2 = (s1 >> 16) | (s1 & 0xFFFF0000u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q4_word_to_f16(cw[(4 * h + j) % kWords], s2, z2, o + 4 * j);
-        } else {
-          const uint32_t s1 = sc[(h >> 1) % kSc];
-          const float sf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 & 0xFFFFu)));
-          const float zf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 >> 16)));
-          if (i & 1) {  // ksteps is even: odd units are the low parts
-#pragma unroll
-            for (int j = 0; j < 4; ++j) q4_word_split<true>(cw[(4 * h + j) % kWords], sf, zf, o + 4 * j);
+    int mine = grp, as = grp;         // the group's next unit, from the chunk's first; its A stage
+    uint32_t i0 = 0, cidx = 0;        // the chunk's first unit; chunks
+    for (int t = 0; t < my_tiles; ++t)
+    for (int c = 0; c < nchunks; ++c, ++cidx) {
+      const int nu = min(kCU, ksteps - c * kCU);
+      const uint32_t sb = cidx % kEtScBufs;
+      const uint8_t* s_chunk = s_mine + sb * F::kScBytes;
+      // also when none of the units is ours: the release below must not run ahead of the fill
+      et_wait_warp(sfull_bar(sb), (cidx / kEtScBufs) & 1u, abort_flag);
+      for (; mine < nu; mine += kEtGroups) {
+        const uint32_t i = i0 + mine;
+        const uint32_t a_dst = a_lane + as * 64;
+        as += kEtGroups;
+        if (as >= tmm.na) as -= tmm.na;
+        // the A stage is free once the unit that had it before is multiplied
+        auto slot_wait = [&]() {
+          const uint32_t j = i - tmm.na;
+          if (i >= static_cast<uint32_t>(tmm.na)) et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag);
+          tc_fence_after();
+        };
+        {
+          const uint32_t w = i % F::kWStages;
+          constexpr int kChunks = F::kWqRowBytes / 16;      // 16 bytes of codes each
+          constexpr int kRegs = FMT == 0 ? 32 : 16;         // f16 pairs of a chunk
+          const uint32_t src = w_mine + w * F::kWBytes;
+          uint32_t sc[FMT == 0 ? 1 : 2];
+          if (FMT == 0) {
+            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + (mine >> 1) * F::kScPitch);
+            sc[0] = mine & 1 ? sc[0] >> 16 : sc[0] & 0xFFFFu;
           } else {
+            const int m2 = SPLIT ? mine >> 1 : mine;
+            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * m2 * F::kScPitch);
+            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * m2 + 1) * F::kScPitch);
+          }
+          et_wait_warp(wfull_bar(w), (i / F::kWStages) & 1u, abort_flag);
+          uint4 cw[kChunks];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q4_word_split<false>(cw[(4 * h + j) % kWords], sf, zf, o + 4 * j);
+          for (int k = 0; k < kChunks; ++k) cw[k] = ld_shared_v4(src + ((k ^ swz) << 4));
+          // the slot is refilled by TMA (the async proxy) once the group has released it
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(wempty_bar(w));
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            const uint32_t wd[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
+            uint32_t o[kRegs];
+            const uint32_t s1 = sc[FMT == 0 ? 0 : k >> 1];
+            const uint32_t s2 = (s1 & 0xFFFFu) | (s1 << 16);
+            if (SPLIT) {
+              const float sf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 & 0xFFFFu)));
+              const float zf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 >> 16)));
+              if (mine & 1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q4_word_split<true>(wd[j], sf, zf, o + 4 * j);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q4_word_split<false>(wd[j], sf, zf, o + 4 * j);
+              }
+            } else if (FMT == 0) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) q2_word_to_f16(wd[j], s2, o + 8 * j);
+            } else {
+              const uint32_t z2 = (s1 >> 16) | (s1 & 0xFFFF0000u);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) q4_word_to_f16(wd[j], s2, z2, o + 4 * j);
+            }
+            if (k == 0) slot_wait();
+            if constexpr (kRegs == 32)
+              tmem_st_32x32b_x32(a_dst + 32 * k, o);
+            else
+              tmem_st_32x32b_x16(a_dst + 16 * k, o);
           }
         }
-        if (h == 0) {
-          // the A stage is free once unit i - kEtA, which had it before, is multiplied
-          const uint32_t j = i - kEtA;
-          if (i >= kEtA && !et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag)) return false;
-          tc_fence_after();
-        }
-        tmem_st_32x32b_x16(a_lane + (i % kEtA) * 64 + 16 * h, o);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full_bar(i & (nx - 1)));
       }
-      tmem_wait_st();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full_bar(i & (nx - 1)));
-      return true;
-    };
-    for (uint32_t i = grp; unit(i, sa) && unit(i + kEtGroups, sb); i += 2 * kEtGroups) {
+      if (lane == 0) mbar_arrive(sempty_bar(sb));
+      mine -= nu;
+      i0 += nu;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -506,14 +547,13 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const EpArgs& a = p.ep;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     uint32_t sc = 0;  // segments done
-    bool ok = true;
     int e = 0;
     auto release = [&](uint32_t ab) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(accempty_bar(ab));
     };
-    for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
       const EtTile tl = et_tile(p, tb, t, e);
       const int n = tl.n0 + 32 * q + lane;       // this thread's weight row
       const bool nv = n < p.N;
@@ -522,16 +562,13 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       if (a.gate && !a.gate_rows && nv) gate_n = bf16_bits_to_f32(a.gate[n]);
       const int chunks = (tl.mt + 15) >> 4;
       // running sum += a segment, in f32 rounded to nearest
-      for (int u = kSeg; SUMS && ok && u < ksteps; u += kSeg, ++sc) {
+      for (int u = kSeg; SUMS && u < ksteps; u += kSeg, ++sc) {
         const uint32_t ab = sc & 1u;
-        if (!et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
+        et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag);
         tc_fence_after();
         for (int cc = set; cc < chunks; cc += 2) {
           uint32_t v[16], w[16];
-          tmem_ld_32x32b_x16(t_lane + ab * kAccCols + 16 * cc, v);
+          tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
           if (u > kSeg) tmem_ld_32x32b_x16(t_lane + kSumCol0 + 16 * cc, w);
           tmem_wait_ld();
           if (u > kSeg) {
@@ -543,12 +580,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         tmem_wait_st();
         release(ab);
       }
-      if (!ok) break;
       const uint32_t ab = sc & 1u;
-      if (!et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag)) {
-        ok = false;
-        break;
-      }
+      et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag);
       ++sc;
       tc_fence_after();
       if (set >= chunks) release(ab);
@@ -574,7 +607,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           }
         }
         uint32_t v[16];
-        tmem_ld_32x32b_x16(t_lane + ab * kAccCols + 16 * cc, v);
+        tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
         float f[16];
         if (SUMS && ksteps > kSeg) {
           uint32_t w[16];
