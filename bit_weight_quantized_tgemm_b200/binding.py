@@ -403,76 +403,114 @@ class _Epilogue(ctypes.Structure):
                 ("gate_rows", _i), ("residual_dtype", _i)]
 
 
-def _out_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.float32:
-        return OUT_F32
-    if t.dtype == torch.bfloat16:
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+class _on_device:
+    """Makes `index` the current device for the C call (free of charge when it already is)."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, index: int):
+        self.ctx = None if _current_device() == index else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _arg(t, dtype, name: str, index: int):
+    """_need, and on CUDA device `index`; the pointer."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _need(t, dtype, name)
+        raise ValueError(f"{name} must be on the same device as the first argument, got {t.device}")
+    return t.data_ptr()
+
+
+def _first(t, dtype, name: str) -> int:
+    """_need for the argument whose device the call runs on; the device's index."""
+    _need(t, dtype, name)
+    return t.get_device()
+
+
+def _out_code(t, name: str) -> int:
+    dt = t.dtype if isinstance(t, torch.Tensor) else None
+    if dt is torch.bfloat16:
         return OUT_BF16
-    raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    if dt is torch.float32:
+        return OUT_F32
+    raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor, got {dt or type(t).__name__}")
 
 
 def _shape(t: torch.Tensor, shape, name: str):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _epilogue(bias, act, gate, residual, M, N, E=None) -> _Epilogue:
+def _epilogue(bias, act, gate, residual, M, N, index, E=None) -> _Epilogue:
     """Checks the epilogue's tensors and fills the C struct; E is set for grouped calls."""
-    ep = _Epilogue(act=act)
+    ep = _Epilogue()
+    ep.act = act
     if bias is not None:
         ep.bias_dtype = _out_code(bias, "bias")
-        _need(bias, bias.dtype, "bias")
+        ep.bias = _arg(bias, bias.dtype, "bias", index)
         _shape(bias, (N,) if E is None else (E, N), "bias")
-        ep.bias = _ptr(bias)
     if gate is not None:
-        _need(gate, torch.bfloat16, "gate")
+        ep.gate = _arg(gate, torch.bfloat16, "gate", index)
         ep.gate_rows = 0 if E is None and gate.dim() == 1 else 1
         _shape(gate, (M, N) if ep.gate_rows else (N,), "gate")
-        ep.gate = _ptr(gate)
     if residual is not None:
         ep.residual_dtype = _out_code(residual, "residual")
-        _need(residual, residual.dtype, "residual")
+        ep.residual = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (M, N), "residual")
-        ep.residual = _ptr(residual)
     return ep
 
 
-def _one_device(*tensors):
-    """The device all the given tensors are on."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
-    return devices.pop()
+def _result(y, like, M, N, out_dtype, index):
+    """The output tensor (a new one, or the caller's y) and its pointer."""
+    if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
+        raise ValueError(f"out_dtype must be OUT_F32 or OUT_BF16, got {out_dtype}")
+    dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+    if y is None:
+        y = like.new_empty((M, N), dtype=dt)
+        return y, y.data_ptr()
+    ptr = _arg(y, dt, "y", index)
+    _shape(y, (M, N), "y")
+    return y, ptr
 
 
-def _call_workspace(need: int, workspace, device):
+def _call_workspace(need: int, workspace, like, index):
     """The caller's workspace, or one of this call's own: the allocator gives it to no other
-    stream or captured graph while this call may still use it."""
+    stream or captured graph while this call may still use it.  (tensor, pointer, bytes)"""
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-        return workspace, workspace.numel()
+        return workspace, _arg(workspace, torch.uint8, "workspace", index), workspace.numel()
     if need == 0:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+        return None, None, 0
+    ws = like.new_empty((need,), dtype=torch.uint8)
+    return ws, ws.data_ptr(), need
 
 
 def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, y, workspace):
-    _need(x, torch.bfloat16, "x")
-    _need(wq, torch.uint8, "wq")
-    _need(sc, torch.float16, "scales")
+    index = _first(x, torch.bfloat16, "x")
+    pw = _arg(wq, torch.uint8, "wq", index)
+    ps = _arg(sc, torch.float16, "scales", index)
     if x.dim() != 2 or wq.dim() != 2:
         raise ValueError("x and wq must have two dimensions")
     M, K = x.shape
     N = wq.shape[0]
     _shape(wq, (N, K // per_byte), "wq")
     _shape(sc, (N, K // 128) if per_byte == 4 else (N, K // 64, 2), "scales")
-    ep = _epilogue(bias, act, gate, residual, M, N)
-    device = _one_device(x, wq, sc, bias, gate, residual, y, workspace)
-    with torch.cuda.device(device):
-        y = _out(y, M, N, out_dtype, device)
-        ws, nbytes = _call_workspace(int(lib().tgemm_ep_workspace_size(op, M, N, K)), workspace, device)
-        _check(getattr(lib(), fn)(_ptr(x), _ptr(wq), _ptr(sc), ctypes.addressof(ep), _ptr(y), M, N, K,
-                                  out_dtype, _ptr(ws), nbytes, _stream()), fn)
+    ep = _epilogue(bias, act, gate, residual, M, N, index)
+    L = lib()
+    with _on_device(index):
+        y, py = _result(y, x, M, N, out_dtype, index)
+        ws, pws, nbytes = _call_workspace(L.tgemm_ep_workspace_size(op, M, N, K), workspace, x, index)
+        _check(getattr(L, fn)(x.data_ptr(), pw, ps, ctypes.addressof(ep), py, M, N, K, out_dtype, pws, nbytes,
+                              _raw_stream(index)), fn)
     return y
 
 
@@ -493,31 +531,30 @@ def gemm_q4_ep(x, wq, sz, *, bias=None, act: int = ACT_NONE, gate=None, residual
 
 
 def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, residual, out_dtype, y, workspace):
-    _need(x, torch.bfloat16, "x")
-    _need(wq, torch.uint8, "wq")
-    _need(sc, torch.float16, "scales")
-    _need(offsets, torch.int32, "offsets")
+    index = _first(x, torch.bfloat16, "x")
+    pw = _arg(wq, torch.uint8, "wq", index)
+    ps = _arg(sc, torch.float16, "scales", index)
+    po = _arg(offsets, torch.int32, "offsets", index)
     if x.dim() != 2 or wq.dim() != 3:
         raise ValueError("x must have two dimensions and wq three")
     x_rows, K = x.shape
-    E, N = wq.shape[:2]
+    E, N = wq.shape[0], wq.shape[1]
     _shape(wq, (E, N, K // per_byte), "wq")
     _shape(sc, (E, N, K // 128) if per_byte == 4 else (E, N, K // 64, 2), "scales")
     _shape(offsets, (E + 1,), "offsets")
-    R = x_rows
+    R, pr = x_rows, None
     if rows is not None:
-        _need(rows, torch.int32, "rows")
+        pr = _arg(rows, torch.int32, "rows", index)
         if rows.dim() != 1:
             raise ValueError("rows must have one dimension")
         R = rows.shape[0]
-    ep = _epilogue(bias, act, gate, residual, R, N, E)
-    device = _one_device(x, wq, sc, offsets, rows, bias, gate, residual, y, workspace)
-    with torch.cuda.device(device):
-        y = _out(y, R, N, out_dtype, device)
-        ws, nbytes = _call_workspace(int(lib().tgemm_grouped_workspace_size(op, R, E, N, K)), workspace, device)
-        _check(getattr(lib(), fn)(_ptr(x), x_rows, _ptr(wq), _ptr(sc), _ptr(offsets), _ptr(rows),
-                                  ctypes.addressof(ep), _ptr(y), R, E, N, K, out_dtype, _ptr(ws), nbytes,
-                                  _stream()), fn)
+    ep = _epilogue(bias, act, gate, residual, R, N, index, E)
+    L = lib()
+    with _on_device(index):
+        y, py = _result(y, x, R, N, out_dtype, index)
+        ws, pws, nbytes = _call_workspace(L.tgemm_grouped_workspace_size(op, R, E, N, K), workspace, x, index)
+        _check(getattr(L, fn)(x.data_ptr(), x_rows, pw, ps, po, pr, ctypes.addressof(ep), py, R, E, N, K, out_dtype,
+                              pws, nbytes, _raw_stream(index)), fn)
     return y
 
 
@@ -547,18 +584,20 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     rows are [offsets[e], offsets[e+1]), rows[r] is the token of sorted row r (-1 behind the
     last), pos[t, j] the sorted row of pair (t, j) (-1 for an id outside [0, experts), whose pair
     is left out).  Pairs of one expert keep their order."""
-    _need(ids, torch.int32, "ids")
+    index = _first(ids, torch.int32, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
+    if experts < 1 or experts > MAX_EXPERTS:
+        raise ValueError(f"experts must be 1 to {MAX_EXPERTS}, got {experts}")
     T, k = ids.shape
-    device = _one_device(ids, workspace)
-    with torch.cuda.device(device):
-        offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=device)
-        rows = torch.empty(T * k, dtype=torch.int32, device=device)
-        pos = torch.empty((T, k), dtype=torch.int32, device=device)
-        ws, nbytes = _call_workspace(int(lib().tgemm_expert_sort_workspace_size(T, k, experts)), workspace, device)
-        _check(lib().tgemm_expert_sort(_ptr(ids), T, k, experts, _ptr(offsets), _ptr(rows), _ptr(pos), _ptr(ws),
-                                       nbytes, _stream()), "tgemm_expert_sort")
+    L = lib()
+    with _on_device(index):
+        offsets = ids.new_empty((experts + 1,))
+        rows = ids.new_empty((T * k,))
+        pos = ids.new_empty((T, k))
+        ws, pws, nbytes = _call_workspace(L.tgemm_expert_sort_workspace_size(T, k, experts), workspace, ids, index)
+        _check(L.tgemm_expert_sort(ids.data_ptr(), T, k, experts, offsets.data_ptr(), rows.data_ptr(),
+                                   pos.data_ptr(), pws, nbytes, _raw_stream(index)), "tgemm_expert_sort")
     return offsets, rows, pos
 
 
@@ -568,24 +607,23 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
     out): h f32 or bf16 [R, N], pos int32 [T, k], weights f32 [T, k], residual f32 or bf16 [T, N].
     f32 sums in the order of j."""
     hd = _out_code(h, "h")
-    _need(h, h.dtype, "h")
-    _need(pos, torch.int32, "pos")
-    _need(weights, torch.float32, "weights")
+    index = _first(h, h.dtype, "h")
+    pp = _arg(pos, torch.int32, "pos", index)
+    pw = _arg(weights, torch.float32, "weights", index)
     if h.dim() != 2 or pos.dim() != 2:
         raise ValueError("h must be [R, N] and pos [T, k]")
     T, k = pos.shape
     R, N = h.shape
     _shape(weights, (T, k), "weights")
-    rd = 0
+    rd, pr = 0, None
     if residual is not None:
         rd = _out_code(residual, "residual")
-        _need(residual, residual.dtype, "residual")
+        pr = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (T, N), "residual")
-    device = _one_device(h, pos, weights, residual, y)
-    with torch.cuda.device(device):
-        y = _out(y, T, N, out_dtype, device)
-        _check(lib().tgemm_expert_combine(_ptr(h), hd, _ptr(pos), _ptr(weights), _ptr(residual), rd, _ptr(y),
-                                          T, k, N, R, out_dtype, _stream()), "tgemm_expert_combine")
+    with _on_device(index):
+        y, py = _result(y, h, T, N, out_dtype, index)
+        _check(lib().tgemm_expert_combine(h.data_ptr(), hd, pp, pw, pr, rd, py, T, k, N, R, out_dtype,
+                                          _raw_stream(index)), "tgemm_expert_combine")
     return y
 
 

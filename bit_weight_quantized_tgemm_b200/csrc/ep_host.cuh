@@ -243,14 +243,15 @@ int run_ep(const EpCall& c) {
 constexpr int64_t kSortMaxPairs = int64_t{1} << 26;
 constexpr int kSortOneCta = 4096;  // pairs one CTA sorts alone
 
-int sort_grid(int64_t n) {
+// CTAs: 2048 pairs each, and no more than keep the table of counts, which every CTA reads, small.
+int sort_grid(int64_t n, int E) {
   if (n <= kSortOneCta) return 1;
-  int64_t g = (n + 4095) / 4096;
-  return static_cast<int>(g > 128 ? 128 : g);
+  const int64_t most = std::max<int64_t>(8, std::min<int64_t>(144, 32768 / E));
+  return static_cast<int>(std::min<int64_t>((n + 2047) / 2048, most));
 }
 
 size_t sort_workspace(int64_t n, int E) {
-  const int G = sort_grid(n);
+  const int G = sort_grid(n, E);
   return G > 1 ? round_up(static_cast<size_t>(G) * E * 4, 256) : 0;
 }
 
@@ -274,11 +275,11 @@ int run_sort(const int* ids, int T, int k, int E, int* offsets, int* rows, int* 
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
     err = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (kSortWarps * kEtMaxExperts + 1) * 4);
+                               (kSortWarps + 2) * kEtMaxExperts * 4);
   });
   if (err != cudaSuccess) return TGEMM_ECUDA;
   const cudaStream_t st = as_stream(stream);
-  const int G = sort_grid(n);
+  const int G = sort_grid(n, E);
   SortParams p;
   p.ids = ids;
   p.offsets = offsets;
@@ -297,7 +298,7 @@ int run_sort(const int* ids, int T, int k, int E, int* offsets, int* rows, int* 
       return e;
   }
   return launch(TGEMM_KIND_PREP, st, [&] {
-    return pdl_launch(sort_place_kernel, G, kSortWarps * 32, (static_cast<size_t>(kSortWarps) * E + 1) * 4, st, p);
+    return pdl_launch(sort_place_kernel, G, kSortWarps * 32, (static_cast<size_t>(kSortWarps) + 2) * E * 4, st, p);
   });
 }
 
@@ -332,10 +333,14 @@ int run_combine(const void* h, int h_dtype, const int* pos, const float* weights
   p.residual_f32 = residual_dtype == TGEMM_OUT_F32;
   p.out_f32 = out_dtype == TGEMM_OUT_F32;
   const cudaStream_t st = as_stream(stream);
-  const int grid = grid_for(static_cast<int64_t>(T) * N, 256, di.sms);
+  const bool vec = N % 8 == 0;
+  const int64_t blocks = (static_cast<int64_t>(T) * (vec ? N / 8 : N) + 255) / 256;
+  if (blocks > INT32_MAX) return TGEMM_ETOOLARGE;
+  const dim3 grid(static_cast<unsigned>(blocks));
   return launch(TGEMM_KIND_PREP, st, [&] {
-    if (h_dtype == TGEMM_OUT_F32) return pdl_launch(combine_kernel<true>, grid, 256, 0, st, p);
-    return pdl_launch(combine_kernel<false>, grid, 256, 0, st, p);
+    if (h_dtype == TGEMM_OUT_F32)
+      return vec ? pdl_launch(combine_kernel<true, 8>, grid, 256, 0, st, p) : pdl_launch(combine_kernel<true, 1>, grid, 256, 0, st, p);
+    return vec ? pdl_launch(combine_kernel<false, 8>, grid, 256, 0, st, p) : pdl_launch(combine_kernel<false, 1>, grid, 256, 0, st, p);
   });
 }
 

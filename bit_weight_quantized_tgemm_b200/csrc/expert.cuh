@@ -28,34 +28,36 @@ __device__ __forceinline__ void sort_run_bounds(const SortParams& p, int cta, in
   hi = static_cast<int>(a + p.run < p.n ? a + p.run : p.n);
 }
 
-// The warp's pairs by expert, added into cnt[e] (the warp's own counters).
-__device__ __forceinline__ void sort_count(const SortParams& p, int lo, int hi, int* cnt) {
+// Four batches of 32 pairs: their experts, -1 past the run's end or outside [0, E).
+__device__ __forceinline__ void sort_load(const SortParams& p, int i0, int hi, int (&id)[4]) {
   const int lane = threadIdx.x & 31;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    int id = i < hi ? __ldg(p.ids + i) : -1;
-    if (id >= p.E) id = -1;
-    if (id < 0) id = -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    if (id >= 0 && lane == __ffs(same) - 1) cnt[id] += __popc(same);
-    __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = i0 + 32 * j + lane;
+    id[j] = i < hi ? __ldg(p.ids + i) : -1;
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (id[j] < 0 || id[j] >= p.E) id[j] = -1;
 }
 
+// Pairs of each CTA by expert.
 __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(const SortParams p) {
   extern __shared__ int st_cnt[];  // [E]
-  pdl_trigger_and_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) st_cnt[e] = 0;
   __syncthreads();
+  pdl_trigger_and_wait();
   int lo, hi;
   sort_run_bounds(p, blockIdx.x, warp, lo, hi);
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    int id = i < hi ? __ldg(p.ids + i) : -1;
-    if (id >= p.E || id < 0) id = -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    if (id >= 0 && lane == __ffs(same) - 1) atomicAdd(st_cnt + id, __popc(same));
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int id[4];
+    sort_load(p, i0, hi, id);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      if (id[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(st_cnt + id[j], __popc(same));
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += blockDim.x)
@@ -64,31 +66,56 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(const SortP
 
 // Places the CTA's pairs.  With one CTA (G = 1) it needs no counts from before.
 __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortParams p) {
-  extern __shared__ int st_base[];  // [warps][E], then the experts' starts [E + 1]
+  extern __shared__ int st_base[];  // [warps][E], then totals [E] and the counts of earlier CTAs [E]
   __shared__ int part[kSortWarps];
-  int* start = st_base + kSortWarps * p.E;
-  pdl_trigger_and_wait();
+  int* s_total = st_base + kSortWarps * p.E;
+  int* s_before = s_total + p.E;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = gridDim.x, g = blockIdx.x;
-  for (int i = tid; i < kSortWarps * p.E; i += blockDim.x) st_base[i] = 0;
+  for (int i = tid; i < (kSortWarps + 2) * p.E; i += blockDim.x) st_base[i] = 0;
   __syncthreads();
-  int lo, hi;
-  sort_run_bounds(p, g, warp, lo, hi);
-  sort_count(p, lo, hi, st_base + warp * p.E);
-  __syncthreads();
-  // E <= blockDim.x: thread e owns expert e
-  int total = 0, before = 0;
-  if (tid < p.E) {
-    if (G > 1) {
-      for (int c = 0; c < G; ++c) {
-        const int v = __ldg(p.hist + static_cast<int64_t>(c) * p.E + tid);
-        total += v;
-        if (c < g) before += v;
+  pdl_trigger_and_wait();
+  if (G > 1) {
+    // every CTA's counts, in whatever order: whole numbers
+    const int n = G * p.E;
+    for (int i0 = tid; i0 < n; i0 += 8 * blockDim.x) {
+      int v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * blockDim.x;
+        v[j] = i < n ? __ldg(p.hist + i) : 0;
       }
-    } else {
-      for (int w = 0; w < kSortWarps; ++w) total += st_base[w * p.E + tid];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * blockDim.x, c = i / p.E, e = i - c * p.E;
+        if (v[j]) {
+          atomicAdd(s_total + e, v[j]);
+          if (c < g) atomicAdd(s_before + e, v[j]);
+        }
+      }
     }
   }
+  int lo, hi;
+  sort_run_bounds(p, g, warp, lo, hi);
+  int* base = st_base + warp * p.E;  // the warp's own counters: no atomics
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int id[4];
+    sort_load(p, i0, hi, id);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      if (id[j] >= 0 && lane == __ffs(same) - 1) base[id[j]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // E <= blockDim.x: thread e owns expert e
+  int mine = 0;
+  if (tid < p.E) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) mine += st_base[w * p.E + tid];
+  }
+  const int total = tid < p.E ? (G > 1 ? s_total[tid] : mine) : 0;
   int incl = total;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
@@ -109,37 +136,40 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
   __syncthreads();
   if (warp > 0) incl += part[warp - 1];
   if (tid < p.E) {
-    int at = incl - total + before;
+    int at = incl - total + s_before[tid];
+#pragma unroll 8
     for (int w = 0; w < kSortWarps; ++w) {
       const int v = st_base[w * p.E + tid];
       st_base[w * p.E + tid] = at;
       at += v;
     }
-    if (tid == p.E - 1) start[0] = incl;  // pairs kept in all
     if (g == 0) {
       p.offsets[tid] = incl - total;
       if (tid == p.E - 1) p.offsets[p.E] = incl;
     }
   }
+  const int kept = part[kSortWarps - 1];
   __syncthreads();
-  int* base = st_base + warp * p.E;
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    int id = i < hi ? __ldg(p.ids + i) : -1;
-    if (id >= p.E || id < 0) id = -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, id);
-    int at = -1;
-    if (id >= 0) at = base[id] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (id >= 0 && lane == __ffs(same) - 1) base[id] += __popc(same);
-    __syncwarp();
-    if (i < hi) {
-      p.pos[i] = at;
-      if (at >= 0) p.rows[at] = i / p.k;
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int id[4];
+    sort_load(p, i0, hi, id);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 32 * j + lane;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      int at = -1;
+      if (id[j] >= 0) at = base[id[j]] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (id[j] >= 0 && lane == __ffs(same) - 1) base[id[j]] += __popc(same);
+      __syncwarp();
+      if (i < hi) {
+        p.pos[i] = at;
+        if (at >= 0) p.rows[at] = i / p.k;
+      }
     }
   }
   // rows behind the last expert's
-  for (int64_t i = start[0] + static_cast<int64_t>(g) * blockDim.x + tid; i < p.n; i += static_cast<int64_t>(G) * blockDim.x)
+  for (int64_t i = kept + static_cast<int64_t>(g) * blockDim.x + tid; i < p.n; i += static_cast<int64_t>(G) * blockDim.x)
     p.rows[i] = -1;
 }
 
@@ -156,27 +186,104 @@ struct CombineParams {
   int residual_f32, out_f32;
 };
 
-template <bool HF32>
+// One thread: V neighbouring columns of one token (V = 8, or 1 where N is no multiple of 8 and
+// the rows of h are not 16-byte aligned).  Up to 8 pairs' rows are on their way at once.
+template <bool HF32, int V>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  constexpr int kB = HF32 && V == 8 ? 4 : 8;  // pairs loaded together
+  const int nv = p.N / V;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   pdl_trigger_and_wait();
-  const int64_t total = static_cast<int64_t>(p.T) * p.N;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += stride) {
-    const int64_t t = i / p.N;
-    const int n = static_cast<int>(i - t * p.N);
-    float v = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int r = __ldg(p.pos + t * p.k + j);
-      if (r < 0 || r >= p.R) continue;
-      v = fmaf(__ldg(p.weights + t * p.k + j), ep_load(p.h, static_cast<int64_t>(r) * p.N + n, HF32), v);
+  if (i >= static_cast<int64_t>(p.T) * nv) return;
+  const int64_t t = i / nv;
+  const int n = static_cast<int>(i - t * nv) * V;
+  const int64_t o = t * p.N + n;
+  const int* pos = p.pos + t * p.k;
+  const float* wts = p.weights + t * p.k;
+  float acc[V];
+#pragma unroll
+  for (int c = 0; c < V; ++c) acc[c] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += kB) {
+    int r[kB];
+    float w[kB];
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+      const bool in = j0 + j < p.k;
+      r[j] = in ? __ldg(pos + j0 + j) : -1;
+      w[j] = in ? __ldg(wts + j0 + j) : 0.f;
+      if (r[j] >= p.R) r[j] = -1;
     }
-    if (p.residual)
-      v += p.residual_f32 ? static_cast<const float*>(p.residual)[i]
-                          : bf16_bits_to_f32(static_cast<const uint16_t*>(p.residual)[i]);
-    if (p.out_f32)
-      static_cast<float*>(p.y)[i] = v;
-    else
-      static_cast<__nv_bfloat16*>(p.y)[i] = __float2bfloat16_rn(v);
+    if (V == 8) {
+      uint4 v[kB][HF32 ? 2 : 1];
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (r[j] >= 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.h) +
+                                                            (static_cast<int64_t>(r[j]) * p.N + n) * (HF32 ? 4 : 2));
+          v[j][0] = __ldg(src);
+          if (HF32) v[j][HF32 ? 1 : 0] = __ldg(src + 1);
+        }
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (r[j] >= 0) {
+          const uint32_t a[4] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w};
+          const uint4 b4 = v[j][HF32 ? 1 : 0];
+          const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (HF32) {
+              acc[c % V] = fmaf(w[j], __uint_as_float(a[c]), acc[c % V]);
+              acc[(4 + c) % V] = fmaf(w[j], __uint_as_float(b[c]), acc[(4 + c) % V]);
+            } else {
+              acc[(2 * c) % V] = fmaf(w[j], __uint_as_float(a[c] << 16), acc[(2 * c) % V]);
+              acc[(2 * c + 1) % V] = fmaf(w[j], __uint_as_float(a[c] & 0xFFFF0000u), acc[(2 * c + 1) % V]);
+            }
+          }
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kB; ++j)
+        if (r[j] >= 0) acc[0] = fmaf(w[j], ep_load(p.h, static_cast<int64_t>(r[j]) * p.N + n, HF32), acc[0]);
+    }
+  }
+  // the residual may be y itself: the same elements, read before they are written
+#pragma unroll
+  for (int c0 = 0; c0 < V; c0 += 4) {
+    if (p.residual) {
+      if (V == 8) {
+        if (p.residual_f32) {
+          const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + o + c0);
+          acc[c0 % V] += r.x;
+          acc[(c0 + 1) % V] += r.y;
+          acc[(c0 + 2) % V] += r.z;
+          acc[(c0 + 3) % V] += r.w;
+        } else {
+          const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) + o + c0);
+          acc[c0 % V] += __uint_as_float(r.x << 16);
+          acc[(c0 + 1) % V] += __uint_as_float(r.x & 0xFFFF0000u);
+          acc[(c0 + 2) % V] += __uint_as_float(r.y << 16);
+          acc[(c0 + 3) % V] += __uint_as_float(r.y & 0xFFFF0000u);
+        }
+      } else {
+        acc[0] += p.residual_f32 ? static_cast<const float*>(p.residual)[o]
+                                 : bf16_bits_to_f32(static_cast<const uint16_t*>(p.residual)[o]);
+      }
+    }
+  }
+  if (V == 8) {
+    if (p.out_f32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.y) + o);
+      dst[0] = make_float4(acc[0], acc[1 % V], acc[2 % V], acc[3 % V]);
+      dst[1] = make_float4(acc[4 % V], acc[5 % V], acc[6 % V], acc[7 % V]);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + o) =
+          make_uint4(pack_bf16x2(acc[0], acc[1 % V]), pack_bf16x2(acc[2 % V], acc[3 % V]),
+                     pack_bf16x2(acc[4 % V], acc[5 % V]), pack_bf16x2(acc[6 % V], acc[7 % V]));
+    }
+  } else if (p.out_f32) {
+    static_cast<float*>(p.y)[o] = acc[0];
+  } else {
+    static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(acc[0]);
   }
 }
 
