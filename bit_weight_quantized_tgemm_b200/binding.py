@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -403,24 +404,16 @@ class _Epilogue(ctypes.Structure):
                 ("gate_rows", _i), ("residual_dtype", _i)]
 
 
+_pack_epilogue = struct.Struct("@PPPiiii").pack  # _Epilogue's bytes
+_bf16, _f16, _f32, _u8, _i32 = torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-class _on_device:
-    """Makes `index` the current device for the C call (free of charge when it already is)."""
-    __slots__ = ("ctx",)
-
-    def __init__(self, index: int):
-        self.ctx = None if _current_device() == index else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on_device(index: int, call):
+    """call() with `index` as the current device."""
+    with torch.cuda.device(index):
+        return call()
 
 
 def _arg(t, dtype, name: str, index: int):
@@ -451,32 +444,31 @@ def _shape(t: torch.Tensor, shape, name: str):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _epilogue(bias, act, gate, residual, M, N, index, E=None) -> _Epilogue:
-    """Checks the epilogue's tensors and fills the C struct; E is set for grouped calls."""
-    ep = _Epilogue()
-    ep.act = act
+def _epilogue(bias, act, gate, residual, M, N, index, E=None):
+    """Checks the epilogue's tensors; the C struct's bytes.  E is set for grouped calls."""
+    pb = pg = pr = bias_dt = gate_rows = res_dt = 0
     if bias is not None:
-        ep.bias_dtype = _out_code(bias, "bias")
-        ep.bias = _arg(bias, bias.dtype, "bias", index)
+        bias_dt = _out_code(bias, "bias")
+        pb = _arg(bias, bias.dtype, "bias", index)
         _shape(bias, (N,) if E is None else (E, N), "bias")
     if gate is not None:
-        ep.gate = _arg(gate, torch.bfloat16, "gate", index)
-        ep.gate_rows = 0 if E is None and gate.dim() == 1 else 1
-        _shape(gate, (M, N) if ep.gate_rows else (N,), "gate")
+        pg = _arg(gate, _bf16, "gate", index)
+        gate_rows = 0 if E is None and gate.dim() == 1 else 1
+        _shape(gate, (M, N) if gate_rows else (N,), "gate")
     if residual is not None:
-        ep.residual_dtype = _out_code(residual, "residual")
-        ep.residual = _arg(residual, residual.dtype, "residual", index)
+        res_dt = _out_code(residual, "residual")
+        pr = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (M, N), "residual")
-    return ep
+    return _pack_epilogue(pb, pg, pr, bias_dt, act, gate_rows, res_dt)
 
 
 def _result(y, like, M, N, out_dtype, index):
     """The output tensor (a new one, or the caller's y) and its pointer."""
     if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
         raise ValueError(f"out_dtype must be OUT_F32 or OUT_BF16, got {out_dtype}")
-    dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+    dt = _bf16 if out_dtype == OUT_BF16 else _f32
     if y is None:
-        y = like.new_empty((M, N), dtype=dt)
+        y = like.new_empty((M, N)) if like.dtype is dt else like.new_empty((M, N), dtype=dt)
         return y, y.data_ptr()
     ptr = _arg(y, dt, "y", index)
     _shape(y, (M, N), "y")
@@ -495,22 +487,27 @@ def _call_workspace(need: int, workspace, like, index):
 
 
 def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, y, workspace):
-    index = _first(x, torch.bfloat16, "x")
-    pw = _arg(wq, torch.uint8, "wq", index)
-    ps = _arg(sc, torch.float16, "scales", index)
+    index = _first(x, _bf16, "x")
+    if _current_device() != index:
+        return _on_device(index, lambda: _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype,
+                                                  y, workspace))
+    pw = _arg(wq, _u8, "wq", index)
+    ps = _arg(sc, _f16, "scales", index)
     if x.dim() != 2 or wq.dim() != 2:
         raise ValueError("x and wq must have two dimensions")
     M, K = x.shape
     N = wq.shape[0]
     _shape(wq, (N, K // per_byte), "wq")
     _shape(sc, (N, K // 128) if per_byte == 4 else (N, K // 64, 2), "scales")
-    ep = _epilogue(bias, act, gate, residual, M, N, index)
-    L = lib()
-    with _on_device(index):
-        y, py = _result(y, x, M, N, out_dtype, index)
-        ws, pws, nbytes = _call_workspace(L.tgemm_ep_workspace_size(op, M, N, K), workspace, x, index)
-        _check(getattr(L, fn)(x.data_ptr(), pw, ps, ctypes.addressof(ep), py, M, N, K, out_dtype, pws, nbytes,
-                              _raw_stream(index)), fn)
+    ep = None
+    if bias is not None or act or gate is not None or residual is not None:
+        ep = _epilogue(bias, act, gate, residual, M, N, index)
+    L = _lib or lib()
+    y, py = _result(y, x, M, N, out_dtype, index)
+    ws, pws, nbytes = _call_workspace(L.tgemm_ep_workspace_size(op, M, N, K), workspace, x, index)
+    st = getattr(L, fn)(x.data_ptr(), pw, ps, ep, py, M, N, K, out_dtype, pws, nbytes, _raw_stream(index))
+    if st:
+        raise TgemmError(st, fn)
     return y
 
 
@@ -531,30 +528,36 @@ def gemm_q4_ep(x, wq, sz, *, bias=None, act: int = ACT_NONE, gate=None, residual
 
 
 def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, residual, out_dtype, y, workspace):
-    index = _first(x, torch.bfloat16, "x")
-    pw = _arg(wq, torch.uint8, "wq", index)
-    ps = _arg(sc, torch.float16, "scales", index)
-    po = _arg(offsets, torch.int32, "offsets", index)
+    index = _first(x, _bf16, "x")
+    if _current_device() != index:
+        return _on_device(index, lambda: _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate,
+                                                       residual, out_dtype, y, workspace))
+    pw = _arg(wq, _u8, "wq", index)
+    ps = _arg(sc, _f16, "scales", index)
+    po = _arg(offsets, _i32, "offsets", index)
     if x.dim() != 2 or wq.dim() != 3:
         raise ValueError("x must have two dimensions and wq three")
     x_rows, K = x.shape
-    E, N = wq.shape[0], wq.shape[1]
+    E, N, kb = wq.shape
     _shape(wq, (E, N, K // per_byte), "wq")
     _shape(sc, (E, N, K // 128) if per_byte == 4 else (E, N, K // 64, 2), "scales")
     _shape(offsets, (E + 1,), "offsets")
     R, pr = x_rows, None
     if rows is not None:
-        pr = _arg(rows, torch.int32, "rows", index)
+        pr = _arg(rows, _i32, "rows", index)
         if rows.dim() != 1:
             raise ValueError("rows must have one dimension")
         R = rows.shape[0]
-    ep = _epilogue(bias, act, gate, residual, R, N, index, E)
-    L = lib()
-    with _on_device(index):
-        y, py = _result(y, x, R, N, out_dtype, index)
-        ws, pws, nbytes = _call_workspace(L.tgemm_grouped_workspace_size(op, R, E, N, K), workspace, x, index)
-        _check(getattr(L, fn)(x.data_ptr(), x_rows, pw, ps, po, pr, ctypes.addressof(ep), py, R, E, N, K, out_dtype,
-                              pws, nbytes, _raw_stream(index)), fn)
+    ep = None
+    if bias is not None or act or gate is not None or residual is not None:
+        ep = _epilogue(bias, act, gate, residual, R, N, index, E)
+    L = _lib or lib()
+    y, py = _result(y, x, R, N, out_dtype, index)
+    ws, pws, nbytes = _call_workspace(L.tgemm_grouped_workspace_size(op, R, E, N, K), workspace, x, index)
+    st = getattr(L, fn)(x.data_ptr(), x_rows, pw, ps, po, pr, ep, py, R, E, N, K, out_dtype, pws, nbytes,
+                        _raw_stream(index))
+    if st:
+        raise TgemmError(st, fn)
     return y
 
 
@@ -584,20 +587,21 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     rows are [offsets[e], offsets[e+1]), rows[r] is the token of sorted row r (-1 behind the
     last), pos[t, j] the sorted row of pair (t, j) (-1 for an id outside [0, experts), whose pair
     is left out).  Pairs of one expert keep their order."""
-    index = _first(ids, torch.int32, "ids")
+    index = _first(ids, _i32, "ids")
+    if _current_device() != index:
+        return _on_device(index, lambda: expert_sort(ids, experts, workspace=workspace))
     if ids.dim() != 2:
         raise ValueError("ids must be [T, k]")
     if experts < 1 or experts > MAX_EXPERTS:
         raise ValueError(f"experts must be 1 to {MAX_EXPERTS}, got {experts}")
     T, k = ids.shape
-    L = lib()
-    with _on_device(index):
-        offsets = ids.new_empty((experts + 1,))
-        rows = ids.new_empty((T * k,))
-        pos = ids.new_empty((T, k))
-        ws, pws, nbytes = _call_workspace(L.tgemm_expert_sort_workspace_size(T, k, experts), workspace, ids, index)
-        _check(L.tgemm_expert_sort(ids.data_ptr(), T, k, experts, offsets.data_ptr(), rows.data_ptr(),
-                                   pos.data_ptr(), pws, nbytes, _raw_stream(index)), "tgemm_expert_sort")
+    L = _lib or lib()
+    offsets = ids.new_empty((experts + 1,))
+    rows = ids.new_empty((T * k,))
+    pos = ids.new_empty((T, k))
+    ws, pws, nbytes = _call_workspace(L.tgemm_expert_sort_workspace_size(T, k, experts), workspace, ids, index)
+    _check(L.tgemm_expert_sort(ids.data_ptr(), T, k, experts, offsets.data_ptr(), rows.data_ptr(),
+                               pos.data_ptr(), pws, nbytes, _raw_stream(index)), "tgemm_expert_sort")
     return offsets, rows, pos
 
 
@@ -608,6 +612,8 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
     f32 sums in the order of j."""
     hd = _out_code(h, "h")
     index = _first(h, h.dtype, "h")
+    if _current_device() != index:
+        return _on_device(index, lambda: expert_combine(h, pos, weights, residual=residual, out_dtype=out_dtype, y=y))
     pp = _arg(pos, torch.int32, "pos", index)
     pw = _arg(weights, torch.float32, "weights", index)
     if h.dim() != 2 or pos.dim() != 2:
@@ -620,10 +626,9 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
         rd = _out_code(residual, "residual")
         pr = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (T, N), "residual")
-    with _on_device(index):
-        y, py = _result(y, h, T, N, out_dtype, index)
-        _check(lib().tgemm_expert_combine(h.data_ptr(), hd, pp, pw, pr, rd, py, T, k, N, R, out_dtype,
-                                          _raw_stream(index)), "tgemm_expert_combine")
+    y, py = _result(y, h, T, N, out_dtype, index)
+    _check(lib().tgemm_expert_combine(h.data_ptr(), hd, pp, pw, pr, rd, py, T, k, N, R, out_dtype,
+                                      _raw_stream(index)), "tgemm_expert_combine")
     return y
 
 

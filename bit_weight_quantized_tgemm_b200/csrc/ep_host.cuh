@@ -82,38 +82,32 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   });
 }
 
-// Small path: the number of warps that share an item, by the rounds of items the GPU's warps
-// need.  An item's end (sums through shared memory, epilogue) costs about two units.
-int es_pick_ks(int64_t items, int U, int warps) {
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int ks = 1; ks <= kEsWarps && (ks == 1 || ks <= U); ks *= 2) {
-    const int64_t cost = (items * ks + warps - 1) / warps * ((U + ks - 1) / ks + 2);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = ks;
-    }
-  }
-  return best;
-}
-
-template <int FMT, int T, int RH>
-int launch_ep_small(EsParams p, int64_t tiles, int sms, cudaStream_t st) {
-  p.tiles_n = (p.N + 16 * RH - 1) / (16 * RH);
-  const int64_t items = tiles * p.tiles_n;
-  if (items > INT32_MAX / 2) return TGEMM_ETOOLARGE;
-  p.KS = es_pick_ks(items, p.U, 2 * sms * kEsWarps);
-  const int groups = kEsWarps / p.KS;
-  const int grid = static_cast<int>(std::min<int64_t>((items + groups - 1) / groups, 2 * sms));
-  const size_t smem = es_smem_bytes(T, p.offsets != nullptr);
-  return launch(FMT == 0 ? TGEMM_KIND_GEMV_Q2 : TGEMM_KIND_GEMV_Q4, st, [&] {
-    return pdl_launch(ep_small_kernel<FMT, T, RH>, grid, kEsWarps * 32, smem, st, p);
-  });
-}
-
 // The most row chunks of `nt` that R rows in E groups can make.
 int64_t max_chunks(int R, int E, int nt) {
   return std::min<int64_t>(R, static_cast<int64_t>(R) / nt + std::min(R, E));
+}
+
+template <int FMT, int T>
+int launch_ep_small(EsParams p, int64_t chunks, int sms, cudaStream_t st) {
+  constexpr int kMost = 225 * 1024, kHalf = 112 * 1024;  // one CTA or two on an SM
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = cudaFuncSetAttribute(ep_small_kernel<FMT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  });
+  if (err != cudaSuccess) return TGEMM_ECUDA;
+  p.tiles_n = (p.N + kEsRows - 1) / kEsRows;
+  const int64_t items = chunks * p.tiles_n;
+  if (items > INT32_MAX / 2) return TGEMM_ETOOLARGE;
+  const bool grouped = p.offsets != nullptr;
+  p.nu_max = (p.U + kEsWarps - 1) / kEsWarps;
+  p.staged = es_smem_bytes(FMT, T, p.nu_max, true, p.E, grouped) <= kMost ? 1 : 0;
+  const int smem = es_smem_bytes(FMT, T, p.nu_max, p.staged != 0, p.E, grouped);
+  if (smem > kMost) return TGEMM_ETOOLARGE;
+  const int grid = static_cast<int>(std::min<int64_t>(items, smem <= kHalf ? 2 * sms : sms));
+  return launch(FMT == 0 ? TGEMM_KIND_GEMV_Q2 : TGEMM_KIND_GEMV_Q4, st, [&] {
+    return pdl_launch(ep_small_kernel<FMT, T>, grid, kEsWarps * 32, static_cast<size_t>(smem), st, p);
+  });
 }
 
 int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
@@ -133,9 +127,8 @@ int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
   const int per = c.offsets ? (c.R + c.E - 1) / c.E : c.R;  // rows of an expert, on average
   auto go = [&](auto fmt_c) {
     constexpr int kF = decltype(fmt_c)::value;
-    if (per <= 8) return launch_ep_small<kF, 1, 2>(p, max_chunks(c.R, c.E, 8), sms, st);
-    if (per <= 16) return launch_ep_small<kF, 2, 2>(p, max_chunks(c.R, c.E, 16), sms, st);
-    return launch_ep_small<kF, 4, 1>(p, max_chunks(c.R, c.E, 32), sms, st);
+    if (per <= 8) return launch_ep_small<kF, 1>(p, max_chunks(c.R, c.E, 8), sms, st);
+    return launch_ep_small<kF, 2>(p, max_chunks(c.R, c.E, 16), sms, st);
   };
   return c.fmt == 0 ? go(std::integral_constant<int, 0>{}) : go(std::integral_constant<int, 1>{});
 }

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(const SortP
     sort_load(p, i0, hi, id);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (i0 + 32 * j >= hi) break;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
       if (id[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(st_cnt + id[j], __popc(same));
     }
@@ -76,23 +77,20 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
   __syncthreads();
   pdl_trigger_and_wait();
   if (G > 1) {
-    // every CTA's counts, in whatever order: whole numbers
-    const int n = G * p.E;
-    for (int i0 = tid; i0 < n; i0 += 8 * blockDim.x) {
-      int v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * blockDim.x;
-        v[j] = i < n ? __ldg(p.hist + i) : 0;
+    // every CTA's counts: thread (seg, e) adds up every nseg-th CTA's; the order does not
+    // matter, they are whole numbers
+    const int ep = (p.E + 31) & ~31, nseg = static_cast<int>(blockDim.x) / ep;
+    const int seg = tid / ep, e = tid - seg * ep;
+    if (seg < nseg && e < p.E) {
+      int sum = 0, before = 0;
+#pragma unroll 8
+      for (int c = seg; c < G; c += nseg) {
+        const int v = __ldg(p.hist + static_cast<int64_t>(c) * p.E + e);
+        sum += v;
+        if (c < g) before += v;
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * blockDim.x, c = i / p.E, e = i - c * p.E;
-        if (v[j]) {
-          atomicAdd(s_total + e, v[j]);
-          if (c < g) atomicAdd(s_before + e, v[j]);
-        }
-      }
+      atomicAdd(s_total + e, sum);
+      atomicAdd(s_before + e, before);
     }
   }
   int lo, hi;
@@ -103,6 +101,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
     sort_load(p, i0, hi, id);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (i0 + 32 * j >= hi) break;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
       if (id[j] >= 0 && lane == __ffs(same) - 1) base[id[j]] += __popc(same);
       __syncwarp();
@@ -155,6 +154,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
     sort_load(p, i0, hi, id);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (i0 + 32 * j >= hi) break;
       const int i = i0 + 32 * j + lane;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
       int at = -1;
