@@ -218,7 +218,7 @@ int run_ep(const EpCall& c) {
   p.tiles_n = (c.N + kEtRows - 1) / kEtRows;
   const int most = out_f32 ? kEtSumTok : kEtTok;  // tokens of a tile
   p.nt = c.offsets ? most : et_pick_nt(c.R, p.tiles_n, most, di.sms);
-  p.ksteps = (c.K + kEtBK - 1) / kEtBK * (split ? 2 : 1);
+  p.ksteps = (c.K + kEtBK - 1) / kEtBK;
   p.nblocks = c.K / (c.fmt == 0 ? 128 : 64);
   p.offsets = c.offsets;
   p.scales = c.scales;

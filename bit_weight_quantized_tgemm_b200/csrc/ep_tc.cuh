@@ -29,15 +29,31 @@ constexpr int kEtXSlots = 8;
 constexpr int kEtChunk = 16;                    // scale blocks of a chunk
 constexpr int kEtScBufs = 3;                    // chunks of scales in shared memory
 constexpr int kEtMaxExperts = 1024;
-// Tensor memory: two accumulators, the running sum if there is one, and from column `a0` the
-// A stages (64 columns each).
+// Tensor memory: two accumulators and from column `a0` the A stages (64 columns each).
 struct EtTmem {
   int acc, a0, na;  // columns of an accumulator, first A column, A stages
 };
-__host__ __device__ constexpr EtTmem et_tmem(bool sums, int nt) {
-  return sums ? EtTmem{kEtSumTok, 256, 4} : nt <= 64 ? EtTmem{64, 128, 6} : EtTmem{128, 256, 4};
+// log2 of the activation slots: 8 of 64 tokens or 4 of 128
+__host__ __device__ constexpr int et_lx(int nt) { return nt <= kEtTok / 2 ? 3 : 2; }
+// The A stages hold no more units than there are activation slots: a dequant group reports unit
+// i on its slot's barrier once it may write its A stages, that is when the unit that had them
+// before is multiplied, and the barrier must then be done with unit i - slots.
+__host__ __device__ constexpr EtTmem et_tmem(bool split, bool sums, int nt) {
+  return split ? EtTmem{kEtSumTok, 160, 5}  // two stages a unit
+         : sums ? EtTmem{kEtSumTok, 160, 4}
+         : nt <= 64 ? EtTmem{64, 128, 6} : EtTmem{128, 256, 4};
 }
-static_assert(3 * kEtSumTok <= 256, "two accumulators and the running sum");
+constexpr bool et_tmem_fits(bool split, bool sums, int nt) {
+  return et_tmem(split, sums, nt).a0 + 64 * et_tmem(split, sums, nt).na <= 512 &&
+         2 * et_tmem(split, sums, nt).acc <= et_tmem(split, sums, nt).a0 &&
+         nt <= et_tmem(split, sums, nt).acc &&
+         et_tmem(split, sums, nt).na / (split ? 2 : 1) <= 1 << et_lx(nt);
+}
+static_assert(et_tmem_fits(false, false, 16) && et_tmem_fits(false, false, 64) && et_tmem_fits(false, false, 80) &&
+                  et_tmem_fits(false, false, 128) && et_tmem_fits(false, true, 16) && et_tmem_fits(false, true, 64) &&
+                  et_tmem_fits(false, true, 80) && et_tmem_fits(true, true, 16) && et_tmem_fits(true, true, 64) &&
+                  et_tmem_fits(true, true, 80),
+              "tensor memory, and units in flight");
 
 template <int FMT>
 struct EtFmt {
@@ -64,7 +80,7 @@ struct EtParams {
   int N, K, E, R;
   int nt;                 // tokens per tile, a multiple of 16
   int tiles_n;            // ceil(N / 128)
-  int ksteps;             // main units per tile: ceil(K / 128), twice that with the low parts
+  int ksteps;             // units (128 k) of a tile: ceil(K / 128)
   int nblocks;            // scale blocks of a row: K / 128 or K / 64
   const int* offsets;     // [E + 1] row ranges, or null: one expert, rows [0, R)
   const uint16_t* scales;
@@ -99,8 +115,10 @@ __device__ __forceinline__ bool elect_one() {
 // Wait for a phase.  The common case is one try_wait (39 cycles); a warp that has to wait
 // sleeps in the barrier unit and leaves its issue slots to others.  Bounded: after
 // kWaitLimitNs it records a timeout and raises the CTA's abort flag, and every later wait of
-// the CTA returns at once, so that the kernel runs out (with the device error word set).
-__device__ __noinline__ void et_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+// the CTA that is not satisfied returns false at once.  A thread whose wait failed issues no
+// more copies or MMAs and arrives on no more barriers, so the kernel runs out with the device
+// error word set.
+__device__ __noinline__ bool et_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     uint32_t ok;
@@ -111,21 +129,23 @@ __device__ __noinline__ void et_wait_slow(uint32_t bar, uint32_t parity, volatil
         : "=r"(ok)
         : "r"(bar), "r"(parity), "r"(100000u)
         : "memory");
-    if (ok || *abort_flag) return;
+    if (ok) return true;
+    if (*abort_flag) return false;
     if (globaltimer_ns() - t0 > kWaitLimitNs) {
       *abort_flag = 1u;
       atomicOr(&g_device_error, kDevErrTimeout);
-      return;
+      return false;
     }
   }
 }
-__device__ __forceinline__ void et_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  if (!mbar_try_wait(bar, parity)) et_wait_slow(bar, parity, abort_flag);
+__device__ __forceinline__ bool et_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  return mbar_try_wait(bar, parity) || et_wait_slow(bar, parity, abort_flag);
 }
-// By a whole warp, which goes on together.
-__device__ __forceinline__ void et_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  et_wait(bar, parity, abort_flag);
+// By a whole warp, which goes on together; each lane gets its own answer.
+__device__ __forceinline__ bool et_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  const bool ok = et_wait(bar, parity, abort_flag);
   __syncwarp();
+  return ok;
 }
 
 // Row ranges and token-tile counts of the experts, in shared memory: off[e], off[e + 1]
@@ -209,39 +229,59 @@ __device__ __forceinline__ void et_build_table(const int* offsets, int E, int R,
   }
 }
 
-// 4-bit codes as an f16 pair: the high part f16(w) or the low part f16(w - f16(w)) of
-// w = (q - z) s in f32.  Pairs as q4_word_to_f16.
-template <bool LOW>
-__device__ __forceinline__ void q4_word_split(uint32_t w, float s, float z, uint32_t* o) {
+__device__ __forceinline__ uint32_t hadd2_u32(uint32_t a, uint32_t b) {
+  __half2 r = __hadd2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hfma2_u32(uint32_t a, uint32_t b, uint32_t c) {
+  __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b), *reinterpret_cast<__half2*>(&c));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// 4-bit weights w = (q - z) s as a high and a low f16 part, pairs as q4_word_to_f16: with
+// t = f16(q - z), hi = f16(t s) and lo = f16(t s - hi), which one fma gives.  EXACT: q - z is an
+// f16 value for every code; otherwise its rounding error (two-sum), times s, joins lo.
+template <bool EXACT>
+__device__ __forceinline__ void q4_word_split(uint32_t w, uint32_t s2, uint32_t z2, uint32_t* hi, uint32_t* lo) {
+  constexpr uint32_t kMagic[2] = {0x64006400u, 0x54005400u};  // 1024, 64
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = (static_cast<float>((w >> (4 * i)) & 15u) - z) * s;
-    const float b = (static_cast<float>((w >> (4 * i + 16)) & 15u) - z) * s;
-    const uint32_t h = pack_f16x2(a, b);
-    if (LOW) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      o[i] = pack_f16x2(a - f.x, b - f.y);
-    } else {
-      o[i] = h;
+    const int j = i & 1;
+    const uint32_t q = hsub2_u32(lop3_and_or(i < 2 ? w : (w >> 8), 0x000F000Fu << (4 * j), kMagic[j]), kMagic[j]);
+    const uint32_t t = hsub2_u32(q, z2);
+    hi[i] = hmul2_u32(t, s2);
+    lo[i] = hfma2_u32(t, s2, hi[i] ^ 0x80008000u);
+    if (!EXACT) {
+      const uint32_t b = hsub2_u32(q, t);  // z, up to rounding
+      const uint32_t err = hadd2_u32(hsub2_u32(q, hadd2_u32(t, b)), hsub2_u32(b, z2));
+      lo[i] = hfma2_u32(err, s2, lo[i]);
     }
   }
 }
+// Whether q - z has at most 11 bits for every code q: z a multiple of 2^-7 in [0, 16], or of
+// 2^-8 (as every f16 is there) in [7, 8].
+__device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
+  const float z = __half2float(__ushort_as_half(static_cast<uint16_t>(z16)));
+  const float z128 = z * 128.f;
+  return (z >= 7.f && z <= 8.f) || (z >= 0.f && z <= 16.f && z128 == rintf(z128));
+}
 
-// SPLIT (4-bit weights, f32 y): every 128-k stage runs twice, with the weights' high and low
-// f16 parts, since f16 weights alone are 2^-12 relative off.
+// SPLIT (4-bit weights, f32 y): a unit's weights are a high and a low f16 part in two A stages,
+// since f16 weights alone are 2^-12 relative off.
 //
 // SUMS (f32 y): the tensor core adds each K = 16 step to the f32 accumulator with truncation,
-// 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every kSeg units the
-// accumulator goes into a running sum in tensor memory, rounded to nearest.
+// 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 32 steps the
+// epilogue warps take the accumulator into running sums in registers, rounded to nearest.  They
+// hold 80 tokens a tile.
 template <int FMT, bool SPLIT, bool SUMS>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
   using F = EtFmt<FMT>;
-  constexpr int kSeg = 4;
-  constexpr int kSumCol0 = 2 * kEtSumTok;
+  constexpr int kSeg = SPLIT ? 2 : 4;    // units of an accumulator segment
+  constexpr int kAU = SPLIT ? 2 : 1;     // A stages of a unit
   static_assert(FMT == 1 || !SPLIT, "ternary weights are exact in f16");
   static_assert(!SPLIT || SUMS, "the low parts are for f32 y");
-  constexpr int kCU = (FMT == 0 ? 16 : 8) * (SPLIT ? 2 : 1);  // main units of a chunk
+  constexpr int kCU = FMT == 0 ? 16 : 8;  // units of a chunk of scales
   extern __shared__ uint8_t et_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(et_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -310,9 +350,9 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const EtTable tb{tab_off, tab_tp};
   const int num_tiles = tab_tp[p.E] * p.tiles_n;
   const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
-  const EtTmem tmm = et_tmem(SUMS, p.nt);
+  const EtTmem tmm = et_tmem(SPLIT, SUMS, p.nt);
   // activation slots: unit i uses slot i & (nx - 1); deeper when the tiles are small
-  const int lx = p.nt <= kEtTok / 2 ? 3 : 2;
+  const int lx = et_lx(p.nt);
   const uint32_t nx = 1u << lx, xslot = kEtXRing >> lx;
 
   // Every role walks the same stream of units: tile by tile, unit by unit along k.
@@ -321,14 +361,16 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     if (elect_one()) {
       uint32_t it = 0;
       int e = 0;
-      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
         for (int u = 0; u < ksteps; ++u, ++it) {
           const uint32_t s = it & (nx - 1);
-          et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
+          ok = et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
           mbar_arrive_expect_tx(full_bar(s), 4096u << box);
-          tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * (SPLIT ? u >> 1 : u));
+          tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * u);
         }
       }
       // every load issued must land before the CTA may exit
@@ -341,7 +383,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       uint32_t it = 0, sc = 0;  // units, accumulator segments
       int as = 0;               // A stage
       int e = 0;
-      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const uint32_t ncols = static_cast<uint32_t>((tl.mt + 15) & ~15);
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
@@ -351,24 +394,29 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           const bool first = u == 0 || (SUMS && u % kSeg == 0);  // of an accumulator segment
           if (first) {
             if (SUMS && u > 0) mma_commit(accfull_bar(sc++ & 1u));
-            et_wait(accempty_bar(sc & 1u), ((sc >> 1) & 1u) ^ 1u, abort_flag);
+            ok = et_wait(accempty_bar(sc & 1u), ((sc >> 1) & 1u) ^ 1u, abort_flag);
+            if (!ok) break;
             d_tmem = tmem_base + (sc & 1u) * tmm.acc;
           }
           const uint32_t s = it & (nx - 1);
-          const uint32_t a_tmem = tmem_base + tmm.a0 + as * 64;
-          if (++as == tmm.na) as = 0;
           const uint32_t xs = sbase + F::kXOff + s * xslot;
           const uint64_t b0 = smem_desc_sw128(xs);
           const uint64_t b1 = smem_desc_sw128(xs + half);
-          et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
+          ok = et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
-                       (kk > 0 || !first) ? 1u : 0u);
+          for (int part = 0; part < kAU; ++part) {
+            const uint32_t a_tmem = tmem_base + tmm.a0 + as * 64;
+            if (++as == tmm.na) as = 0;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
+                         (part > 0 || kk > 0 || !first) ? 1u : 0u);
+          }
           mma_commit(empty_bar(s));
         }
-        mma_commit(accfull_bar(sc++ & 1u));
+        if (ok) mma_commit(accfull_bar(sc++ & 1u));
       }
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0u);
@@ -378,15 +426,17 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     if (elect_one()) {
       uint32_t it = 0;
       int e = 0;
-      for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int row = tl.e * p.N + tl.n0;
         for (int u = 0; u < ksteps; ++u, ++it) {
           const uint32_t w = it % F::kWStages;
-          et_wait(wempty_bar(w), ((it / F::kWStages) & 1u) ^ 1u, abort_flag);
+          ok = et_wait(wempty_bar(w), ((it / F::kWStages) & 1u) ^ 1u, abort_flag);
+          if (!ok) break;
           mbar_arrive_expect_tx(wfull_bar(w), F::kWBytes);
           tma_load_2d(sbase + F::kWOff + w * F::kWBytes, &tm.w, wfull_bar(w),
-                      (SPLIT ? u >> 1 : u) * F::kWqRowBytes, row);
+                      u * F::kWqRowBytes, row);
         }
       }
       for (uint32_t j = (it > F::kWStages ? it - F::kWStages : 0); j < it; ++j)
@@ -404,6 +454,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const bool words = FMT == 1 || ((p.nblocks & 1) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3) == 0);
     uint32_t cidx = 0;
     int e = 0;
+    bool ok = true;
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
       const EtTile tl = et_tile(p, tb, t, e);
       const int rows = min(kEtRows, p.N - tl.n0);
@@ -412,7 +463,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         const uint32_t b = cidx % kEtScBufs;
         const int k = c * kEtChunk + wd * (kEtChunk / kW);  // the word's (first) block
         const uint32_t off = F::kScOff + b * F::kScBytes + wd * F::kScPitch + 4 * rl;
-        et_wait_warp(sempty_bar(b), ((cidx / kEtScBufs) & 1u) ^ 1u, abort_flag);
+        ok = et_wait_warp(sempty_bar(b), ((cidx / kEtScBufs) & 1u) ^ 1u, abort_flag) && ok;
+        if (!ok) continue;
         if (words) {
           // rows past N and blocks past K: zeros, no weight
           const uint32_t* src = reinterpret_cast<const uint32_t*>(p.scales) + (row0 * p.nblocks + k) / (FMT == 0 ? 2 : 1);
@@ -455,24 +507,34 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
     const int my_tiles = num_tiles > static_cast<int>(blockIdx.x)
                              ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
-    int mine = grp, as = grp;         // the group's next unit, from the chunk's first; its A stage
+    int mine = grp, as = grp * kAU % tmm.na;  // the group's next unit, from the chunk's first; its A stage
     uint32_t i0 = 0, cidx = 0;        // the chunk's first unit; chunks
+    bool ok = true;
     for (int t = 0; t < my_tiles; ++t)
     for (int c = 0; c < nchunks; ++c, ++cidx) {
       const int nu = min(kCU, ksteps - c * kCU);
       const uint32_t sb = cidx % kEtScBufs;
       const uint8_t* s_chunk = s_mine + sb * F::kScBytes;
       // also when none of the units is ours: the release below must not run ahead of the fill
-      et_wait_warp(sfull_bar(sb), (cidx / kEtScBufs) & 1u, abort_flag);
+      ok = et_wait_warp(sfull_bar(sb), (cidx / kEtScBufs) & 1u, abort_flag) && ok;
       for (; mine < nu; mine += kEtGroups) {
         const uint32_t i = i0 + mine;
-        const uint32_t a_dst = a_lane + as * 64;
-        as += kEtGroups;
-        if (as >= tmm.na) as -= tmm.na;
-        // the A stage is free once the unit that had it before is multiplied
+        uint32_t a_dst[kAU];
+#pragma unroll
+        for (int part = 0; part < kAU; ++part) {
+          const int sl = as + part;
+          a_dst[part] = a_lane + (sl >= tmm.na ? sl - tmm.na : sl) * 64;
+        }
+        as += kEtGroups * kAU;
+        while (as >= tmm.na) as -= tmm.na;
+        // The unit's A stages are free once the units that had them before are multiplied; the
+        // last of those is unit (kAU i + kAU - 1 - na) / kAU.
         auto slot_wait = [&]() {
-          const uint32_t j = i - tmm.na;
-          if (i >= static_cast<uint32_t>(tmm.na)) et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag);
+          const uint32_t before = kAU * i + kAU - 1;
+          if (before >= static_cast<uint32_t>(tmm.na)) {
+            const uint32_t j = (before - tmm.na) / kAU;
+            ok = et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag) && ok;
+          }
           tc_fence_after();
         };
         {
@@ -485,33 +547,34 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + (mine >> 1) * F::kScPitch);
             sc[0] = mine & 1 ? sc[0] >> 16 : sc[0] & 0xFFFFu;
           } else {
-            const int m2 = SPLIT ? mine >> 1 : mine;
-            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * m2 * F::kScPitch);
-            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * m2 + 1) * F::kScPitch);
+            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * mine * F::kScPitch);
+            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * mine + 1) * F::kScPitch);
           }
-          et_wait_warp(wfull_bar(w), (i / F::kWStages) & 1u, abort_flag);
+          const bool exact = SPLIT && __all_sync(0xFFFFFFFFu, q4_zero_exact(sc[0] >> 16) && q4_zero_exact(sc[FMT == 0 ? 0 : 1] >> 16));
+          ok = et_wait_warp(wfull_bar(w), (i / F::kWStages) & 1u, abort_flag) && ok;
           uint4 cw[kChunks];
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) cw[k] = ld_shared_v4(src + ((k ^ swz) << 4));
           // the slot is refilled by TMA (the async proxy) once the group has released it
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(wempty_bar(w));
+          if (lane == 0 && ok) mbar_arrive(wempty_bar(w));
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
             const uint32_t wd[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
             uint32_t o[kRegs];
             const uint32_t s1 = sc[FMT == 0 ? 0 : k >> 1];
             const uint32_t s2 = (s1 & 0xFFFFu) | (s1 << 16);
-            if (SPLIT) {
-              const float sf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 & 0xFFFFu)));
-              const float zf = __half2float(__ushort_as_half(static_cast<uint16_t>(s1 >> 16)));
-              if (mine & 1) {
+            uint32_t lo[SPLIT ? kRegs : 1];
+            (void)lo;
+            if constexpr (SPLIT) {
+              const uint32_t z2 = (s1 >> 16) | (s1 & 0xFFFF0000u);
+              if (exact) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q4_word_split<true>(wd[j], sf, zf, o + 4 * j);
+                for (int j = 0; j < 4; ++j) q4_word_split<true>(wd[j], s2, z2, o + 4 * j, lo + 4 * j);
               } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q4_word_split<false>(wd[j], sf, zf, o + 4 * j);
+                for (int j = 0; j < 4; ++j) q4_word_split<false>(wd[j], s2, z2, o + 4 * j, lo + 4 * j);
               }
             } else if (FMT == 0) {
 #pragma unroll
@@ -523,18 +586,19 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             }
             if (k == 0) slot_wait();
             if constexpr (kRegs == 32)
-              tmem_st_32x32b_x32(a_dst + 32 * k, o);
+              tmem_st_32x32b_x32(a_dst[0] + 32 * k, o);
             else
-              tmem_st_32x32b_x16(a_dst + 16 * k, o);
+              tmem_st_32x32b_x16(a_dst[0] + 16 * k, o);
+            if constexpr (SPLIT) tmem_st_32x32b_x16(a_dst[kAU - 1] + 16 * k, lo);
           }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full_bar(i & (nx - 1)));
+        if (lane == 0 && ok) mbar_arrive(full_bar(i & (nx - 1)));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(sempty_bar(sb));
+      if (lane == 0 && ok) mbar_arrive(sempty_bar(sb));
       mine -= nu;
       i0 += nu;
     }
@@ -547,11 +611,12 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const EpArgs& a = p.ep;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     uint32_t sc = 0;  // segments done
+    bool ok = true;
     int e = 0;
     auto release = [&](uint32_t ab) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(accempty_bar(ab));
+      if (lane == 0 && ok) mbar_arrive(accempty_bar(ab));
     };
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
       const EtTile tl = et_tile(p, tb, t, e);
@@ -560,93 +625,99 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       float bias = 0.f, gate_n = 1.f;
       if (a.bias && nv) bias = ep_load(a.bias, static_cast<int64_t>(tl.e) * p.N + n, a.bias_f32);
       if (a.gate && !a.gate_rows && nv) gate_n = bf16_bits_to_f32(a.gate[n]);
-      const int chunks = (tl.mt + 15) >> 4;
-      // running sum += a segment, in f32 rounded to nearest
-      for (int u = kSeg; SUMS && u < ksteps; u += kSeg, ++sc) {
-        const uint32_t ab = sc & 1u;
-        et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag);
-        tc_fence_after();
-        for (int cc = set; cc < chunks; cc += 2) {
-          uint32_t v[16], w[16];
-          tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
-          if (u > kSeg) tmem_ld_32x32b_x16(t_lane + kSumCol0 + 16 * cc, w);
-          tmem_wait_ld();
-          if (u > kSeg) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
-          }
-          tmem_st_32x32b_x16(t_lane + kSumCol0 + 16 * cc, v);
-        }
-        tmem_wait_st();
-        release(ab);
-      }
-      const uint32_t ab = sc & 1u;
-      et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag);
-      ++sc;
-      tc_fence_after();
-      if (set >= chunks) release(ab);
-      for (int cc = set; cc < chunks; cc += 2) {
-        const int mt = tl.mt - 16 * cc;  // tokens of the chunk, at least one
-        const int64_t i0 = static_cast<int64_t>(tl.m0 + 16 * cc) * p.N + n;
+      // The outputs of n tokens from token 16 or 8 cc of the tile on: f holds their sums.
+      auto finish = [&](auto& f, int m, auto&& sums) {
+        constexpr int kN = sizeof(f) / sizeof(float);
+        const int mt = tl.mt - m;  // at least one
+        const int64_t i0 = static_cast<int64_t>(tl.m0 + m) * p.N + n;
         // the tokens' gates and residuals, on their way while the sums are read
-        float g[16], r[16];
+        float g[kN], r[kN];
         if (a.gate && a.gate_rows) {
           const uint16_t* src = a.gate + i0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, src += p.N) g[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
+          for (int i = 0; i < kN; ++i, src += p.N) g[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
         }
         if (a.residual) {
           if (a.residual_f32) {
             const float* src = static_cast<const float*>(a.residual) + i0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i, src += p.N) r[i] = nv && i < mt ? *src : 0.f;
+            for (int i = 0; i < kN; ++i, src += p.N) r[i] = nv && i < mt ? *src : 0.f;
           } else {
             const uint16_t* src = static_cast<const uint16_t*>(a.residual) + i0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i, src += p.N) r[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
+            for (int i = 0; i < kN; ++i, src += p.N) r[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
           }
         }
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
-        float f[16];
-        if (SUMS && ksteps > kSeg) {
-          uint32_t w[16];
-          tmem_ld_32x32b_x16(t_lane + kSumCol0 + 16 * cc, w);
-          tmem_wait_ld();
+        sums();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]) + __uint_as_float(v[i]);
-        } else {
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
-        }
-        if (cc + 2 >= chunks) release(ab);  // the accumulator is read out
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] += bias;
+        for (int i = 0; i < kN; ++i) f[i] += bias;
         ep_act_all(f, a.act);
         if (a.gate) {
-          if (a.gate_rows) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] *= g[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] *= gate_n;
-          }
+          for (int i = 0; i < kN; ++i) f[i] *= a.gate_rows ? g[i] : gate_n;
         }
         if (a.residual) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] += r[i];
+          for (int i = 0; i < kN; ++i) f[i] += r[i];
         }
         if (a.out_f32) {
           float* dst = static_cast<float*>(a.y) + i0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, dst += p.N)
+          for (int i = 0; i < kN; ++i, dst += p.N)
             if (nv && i < mt) *dst = f[i];
         } else {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.y) + i0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i, dst += p.N)
+          for (int i = 0; i < kN; ++i, dst += p.N)
             if (nv && i < mt) *dst = __float2bfloat16_rn(f[i]);
+        }
+      };
+      if constexpr (SUMS) {
+        // 8-token chunks of this set's parity: running sum += a segment, rounded to nearest
+        constexpr int kMine = kEtSumTok / 16;
+        const int chunks = (tl.mt + 7) >> 3;
+        float sum[kMine][8];
+#pragma unroll
+        for (int k = 0; k < kMine; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[k][i] = 0.f;
+        for (int u = 0; u < ksteps; u += kSeg, ++sc) {
+          const uint32_t ab = sc & 1u;
+          ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kMine; ++k) {
+            if (2 * k + set >= chunks) break;
+            uint32_t v[8];
+            tmem_ld_32x32b_x8(t_lane + ab * tmm.acc + 8 * (2 * k + set), v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[k][i] += __uint_as_float(v[i]);
+          }
+          release(ab);
+        }
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          if (2 * k + set >= chunks) break;
+          finish(sum[k], 8 * (2 * k + set), [] {});
+        }
+      } else {
+        const int chunks = (tl.mt + 15) >> 4;
+        const uint32_t ab = sc & 1u;
+        ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
+        ++sc;
+        tc_fence_after();
+        if (set >= chunks) release(ab);
+        for (int cc = set; cc < chunks; cc += 2) {
+          float f[16];
+          finish(f, 16 * cc, [&] {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
+            tmem_wait_ld();
+            if (cc + 2 >= chunks) release(ab);  // the accumulator is read out
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+          });
         }
       }
     }
