@@ -62,7 +62,10 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (int e = encoder(&enc)) return e;
   for (int i = 0; i < 4; ++i) {
-    if (i > 0 && (8 << i) >= p.nt) break;  // no tile is that large
+    // the boxes that tiles of up to nt tokens use; a dense call has full tiles and one rest
+    const int lo = i ? 8 << i : 0, hi = 16 << i, rest = c.R % p.nt;
+    const bool used = c.offsets ? lo < p.nt : (c.R >= p.nt && p.nt > lo && p.nt <= hi) || (rest > lo && rest <= hi);
+    if (!used) continue;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.K) * 2, 128};
     const cuuint32_t box[3] = {64, 16u << i, 2};

@@ -24,8 +24,8 @@ constexpr int kEtScaleWarp = 3;
 constexpr int kEtDeqWarp0 = 4;
 constexpr int kEtEpiWarp0 = kEtDeqWarp0 + 4 * kEtGroups;
 constexpr int kEtThreads = (kEtEpiWarp0 + 8) * 32;
-constexpr int kEtXRing = 4 * kEtTok * 256;      // activation ring: 4 slots of 128 tokens or 8 of 64
-constexpr int kEtXSlots = 8;
+constexpr int kEtXRing = 5 * kEtTok * 256;      // activation ring: 5 slots of 128 tokens or 10 of 64
+constexpr int kEtXSlots = 10;
 constexpr int kEtChunk = 16;                    // scale blocks of a chunk
 constexpr int kEtScBufs = 3;                    // chunks of scales in shared memory
 constexpr int kEtMaxExperts = 1024;
@@ -33,21 +33,21 @@ constexpr int kEtMaxExperts = 1024;
 struct EtTmem {
   int acc, a0, na;  // columns of an accumulator, first A column, A stages
 };
-// log2 of the activation slots: 8 of 64 tokens or 4 of 128
-__host__ __device__ constexpr int et_lx(int nt) { return nt <= kEtTok / 2 ? 3 : 2; }
+// activation slots
+__host__ __device__ constexpr int et_nx(int nt) { return nt <= kEtTok / 2 ? 10 : 5; }
 // The A stages hold no more units than there are activation slots: a dequant group reports unit
 // i on its slot's barrier once it may write its A stages, that is when the unit that had them
 // before is multiplied, and the barrier must then be done with unit i - slots.
 __host__ __device__ constexpr EtTmem et_tmem(bool split, bool sums, int nt) {
   return split ? EtTmem{kEtSumTok, 160, 5}  // two stages a unit
-         : sums ? EtTmem{kEtSumTok, 160, 4}
+         : sums ? EtTmem{kEtSumTok, 160, 5}
          : nt <= 64 ? EtTmem{64, 128, 6} : EtTmem{128, 256, 4};
 }
 constexpr bool et_tmem_fits(bool split, bool sums, int nt) {
   return et_tmem(split, sums, nt).a0 + 64 * et_tmem(split, sums, nt).na <= 512 &&
          2 * et_tmem(split, sums, nt).acc <= et_tmem(split, sums, nt).a0 &&
          nt <= et_tmem(split, sums, nt).acc &&
-         et_tmem(split, sums, nt).na / (split ? 2 : 1) <= 1 << et_lx(nt);
+         et_tmem(split, sums, nt).na / (split ? 2 : 1) <= et_nx(nt);
 }
 static_assert(et_tmem_fits(false, false, 16) && et_tmem_fits(false, false, 64) && et_tmem_fits(false, false, 80) &&
                   et_tmem_fits(false, false, 128) && et_tmem_fits(false, true, 16) && et_tmem_fits(false, true, 64) &&
@@ -58,7 +58,7 @@ static_assert(et_tmem_fits(false, false, 16) && et_tmem_fits(false, false, 64) &
 template <int FMT>
 struct EtFmt {
   static constexpr int kWqRowBytes = FMT == 0 ? 32 : 64;
-  static constexpr int kWStages = FMT == 0 ? 16 : 8;
+  static constexpr int kWStages = FMT == 0 ? 8 : 4;
   static constexpr int kWBytes = kEtRows * kWqRowBytes;
   static constexpr int kXOff = 0;
   static constexpr int kWOff = kEtXRing;
@@ -351,36 +351,39 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const int num_tiles = tab_tp[p.E] * p.tiles_n;
   const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
   const EtTmem tmm = et_tmem(SPLIT, SUMS, p.nt);
-  // activation slots: unit i uses slot i & (nx - 1); deeper when the tiles are small
-  const int lx = et_lx(p.nt);
-  const uint32_t nx = 1u << lx, xslot = kEtXRing >> lx;
+  // activation slots: unit i uses slot i % nx, for the (i / nx)-th time
+  const uint32_t nx = et_nx(p.nt), xslot = kEtXRing / nx;
 
   // Every role walks the same stream of units: tile by tile, unit by unit along k.
   if (warp == 0) {
     // ------------------------------------------------------------ activation producer
     if (elect_one()) {
-      uint32_t it = 0;
+      uint32_t it = 0, s = 0, ph = 0;
       int e = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
-        for (int u = 0; u < ksteps; ++u, ++it) {
-          const uint32_t s = it & (nx - 1);
-          ok = et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
+        for (int u = 0; u < ksteps; ++u) {
+          ok = et_wait(empty_bar(s), ph ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(full_bar(s), 4096u << box);
           tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * u);
+          ++it;
+          if (++s == nx) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
       // every load issued must land before the CTA may exit
       for (uint32_t j = (it > nx ? it - nx : 0); j < it; ++j)
-        mbar_wait_drain(full_bar(j & (nx - 1)), (j >> lx) & 1u);
+        mbar_wait_drain(full_bar(j % nx), (j / nx) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
-      uint32_t it = 0, sc = 0;  // units, accumulator segments
+      uint32_t s = 0, ph = 0, sc = 0;  // activation slot and its phase, accumulator segments
       int as = 0;               // A stage
       int e = 0;
       bool ok = true;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
         const uint32_t half = 2048u << et_box(tl.mt);  // bytes of a k block's box
         uint32_t d_tmem = 0;
-        for (int u = 0; u < ksteps; ++u, ++it) {
+        for (int u = 0; u < ksteps; ++u) {
           const bool first = u == 0 || (SUMS && u % kSeg == 0);  // of an accumulator segment
           if (first) {
             if (SUMS && u > 0) mma_commit(accfull_bar(sc++ & 1u));
@@ -398,11 +401,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             if (!ok) break;
             d_tmem = tmem_base + (sc & 1u) * tmm.acc;
           }
-          const uint32_t s = it & (nx - 1);
           const uint32_t xs = sbase + F::kXOff + s * xslot;
           const uint64_t b0 = smem_desc_sw128(xs);
           const uint64_t b1 = smem_desc_sw128(xs + half);
-          ok = et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
+          ok = et_wait(full_bar(s), ph, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -415,6 +417,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
                          (part > 0 || kk > 0 || !first) ? 1u : 0u);
           }
           mma_commit(empty_bar(s));
+          if (++s == nx) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
         if (ok) mma_commit(accfull_bar(sc++ & 1u));
       }
@@ -509,6 +515,12 @@ __global__ void __launch_bounds__(kEtThreads, 1)
                              ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
     int mine = grp, as = grp * kAU % tmm.na;  // the group's next unit, from the chunk's first; its A stage
     uint32_t i0 = 0, cidx = 0;        // the chunk's first unit; chunks
+    uint32_t xs = grp;                // the unit's activation slot
+    // the last unit that had the unit's A stages before is `back` units earlier; jr: its place
+    // in two rounds of the activation slots
+    const uint32_t back = (tmm.na - (kAU - 1)) / kAU;
+    uint32_t jr = grp + 2 * nx - back;
+    if (jr >= 2 * nx) jr -= 2 * nx;
     bool ok = true;
     for (int t = 0; t < my_tiles; ++t)
     for (int c = 0; c < nchunks; ++c, ++cidx) {
@@ -527,15 +539,13 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         }
         as += kEtGroups * kAU;
         while (as >= tmm.na) as -= tmm.na;
-        // The unit's A stages are free once the units that had them before are multiplied; the
-        // last of those is unit (kAU i + kAU - 1 - na) / kAU.
+        // the unit's A stages are free once the units that had them before are multiplied
         auto slot_wait = [&]() {
-          const uint32_t before = kAU * i + kAU - 1;
-          if (before >= static_cast<uint32_t>(tmm.na)) {
-            const uint32_t j = (before - tmm.na) / kAU;
-            ok = et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag) && ok;
-          }
+          if (i >= back)
+            ok = et_wait_warp(empty_bar(jr >= nx ? jr - nx : jr), jr >= nx ? 1u : 0u, abort_flag) && ok;
           tc_fence_after();
+          jr += kEtGroups;
+          if (jr >= 2 * nx) jr -= 2 * nx;
         };
         {
           const uint32_t w = i % F::kWStages;
@@ -595,7 +605,9 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(full_bar(i & (nx - 1)));
+        if (lane == 0 && ok) mbar_arrive(full_bar(xs));
+        xs += kEtGroups;
+        if (xs >= nx) xs -= nx;
       }
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(sempty_bar(sb));
