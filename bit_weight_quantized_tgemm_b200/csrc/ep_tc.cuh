@@ -637,27 +637,44 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       float bias = 0.f, gate_n = 1.f;
       if (a.bias && nv) bias = ep_load(a.bias, static_cast<int64_t>(tl.e) * p.N + n, a.bias_f32);
       if (a.gate && !a.gate_rows && nv) gate_n = bf16_bits_to_f32(a.gate[n]);
-      // The outputs of n tokens from token 16 or 8 cc of the tile on: f holds their sums.
+      // While the tile is multiplied, its gates and residuals come into L2: a lane a token, this
+      // warp's 32 weight rows (64 or 128 bytes), tokens shared between the two sets.
+      if (n - lane < p.N) {
+        for (int k = lane + 32 * set; k < tl.mt; k += 64) {
+          const int64_t i = static_cast<int64_t>(tl.m0 + k) * p.N + n - lane;
+          if (a.gate && a.gate_rows) prefetch_l2(a.gate + i);
+          if (a.residual)
+            prefetch_l2(a.residual_f32 ? static_cast<const void*>(static_cast<const float*>(a.residual) + i)
+                                       : static_cast<const void*>(static_cast<const uint16_t*>(a.residual) + i));
+        }
+      }
+      // The outputs of the kN tokens from token m of the tile on, whose sums f gets from sums().
+      // Loads are unconditional, from clamped places: a load behind a branch of its own is waited
+      // for before the next one (13000 cycles a chunk instead of 700).  bf16 outputs leave in
+      // pairs: neighbouring lanes trade, so that one has (n, n + 1) of an even token and the
+      // other of the odd one.
       auto finish = [&](auto& f, int m, auto&& sums) {
         constexpr int kN = sizeof(f) / sizeof(float);
-        const int mt = tl.mt - m;  // at least one
-        const int64_t i0 = static_cast<int64_t>(tl.m0 + m) * p.N + n;
-        // the tokens' gates and residuals, on their way while the sums are read
-        float g[kN], r[kN];
+        const int mt = min(kN, tl.mt - m);
+        const int64_t row0 = static_cast<int64_t>(tl.m0 + m) * p.N;
+        const int64_t i0 = row0 + (nv ? n : p.N - 1);
+        auto at = [&](int i) { return static_cast<uint32_t>(min(i, mt - 1)) * static_cast<uint32_t>(p.N); };
+        uint16_t g[kN];
+        uint32_t r[kN];
         if (a.gate && a.gate_rows) {
           const uint16_t* src = a.gate + i0;
 #pragma unroll
-          for (int i = 0; i < kN; ++i, src += p.N) g[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
+          for (int i = 0; i < kN; ++i) g[i] = src[at(i)];
         }
         if (a.residual) {
           if (a.residual_f32) {
-            const float* src = static_cast<const float*>(a.residual) + i0;
+            const uint32_t* src = static_cast<const uint32_t*>(a.residual) + i0;
 #pragma unroll
-            for (int i = 0; i < kN; ++i, src += p.N) r[i] = nv && i < mt ? *src : 0.f;
+            for (int i = 0; i < kN; ++i) r[i] = src[at(i)];
           } else {
             const uint16_t* src = static_cast<const uint16_t*>(a.residual) + i0;
 #pragma unroll
-            for (int i = 0; i < kN; ++i, src += p.N) r[i] = nv && i < mt ? bf16_bits_to_f32(*src) : 0.f;
+            for (int i = 0; i < kN; ++i) r[i] = src[at(i)];
           }
         }
         sums();
@@ -665,23 +682,58 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         for (int i = 0; i < kN; ++i) f[i] += bias;
         ep_act_all(f, a.act);
         if (a.gate) {
+          if (a.gate_rows) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) f[i] *= a.gate_rows ? g[i] : gate_n;
+            for (int i = 0; i < kN; ++i) f[i] *= bf16_bits_to_f32(g[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) f[i] *= gate_n;
+          }
         }
         if (a.residual) {
+          if (a.residual_f32) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) f[i] += r[i];
+            for (int i = 0; i < kN; ++i) f[i] += __uint_as_float(r[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) f[i] += __uint_as_float(r[i] << 16);
+          }
         }
         if (a.out_f32) {
           float* dst = static_cast<float*>(a.y) + i0;
+          if (nv && mt == kN) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i, dst += p.N)
-            if (nv && i < mt) *dst = f[i];
-        } else {
+            for (int i = 0; i < kN; ++i) dst[static_cast<uint32_t>(i) * static_cast<uint32_t>(p.N)] = f[i];
+          } else if (nv) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (i < mt) dst[at(i)] = f[i];
+          }
+        } else if ((p.N & 1) == 0) {
+          const int odd = lane & 1;
+          uint32_t v[kN / 2];
+#pragma unroll
+          for (int i = 0; i < kN / 2; ++i) {
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f[2 * i] : f[2 * i + 1], 1);
+            v[i] = odd ? pack_bf16x2(got, f[2 * i + 1]) : pack_bf16x2(f[2 * i], got);
+          }
+          // both lanes of a pair are inside N, or neither
+          uint16_t* dst = static_cast<uint16_t*>(a.y) + row0 + (n - odd) + (odd ? p.N : 0);
+          if (nv && mt == kN) {
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i)
+              *reinterpret_cast<uint32_t*>(dst + static_cast<uint32_t>(2 * i) * static_cast<uint32_t>(p.N)) = v[i];
+          } else if (nv) {
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i)
+              if (2 * i + odd < mt)
+                *reinterpret_cast<uint32_t*>(dst + static_cast<uint32_t>(2 * i) * static_cast<uint32_t>(p.N)) = v[i];
+          }
+        } else if (nv) {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.y) + i0;
 #pragma unroll
-          for (int i = 0; i < kN; ++i, dst += p.N)
-            if (nv && i < mt) *dst = __float2bfloat16_rn(f[i]);
+          for (int i = 0; i < kN; ++i)
+            if (i < mt) dst[at(i)] = __float2bfloat16_rn(f[i]);
         }
       };
       if constexpr (SUMS) {
@@ -716,13 +768,18 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       } else {
         const int chunks = (tl.mt + 15) >> 4;
         const uint32_t ab = sc & 1u;
-        ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
-        ++sc;
-        tc_fence_after();
-        if (set >= chunks) release(ab);
+        auto accumulated = [&] {
+          ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
+          tc_fence_after();
+        };
+        if (set >= chunks) {
+          accumulated();
+          release(ab);
+        }
         for (int cc = set; cc < chunks; cc += 2) {
           float f[16];
           finish(f, 16 * cc, [&] {
+            if (cc == set) accumulated();  // the first chunk's operands are on their way already
             uint32_t v[16];
             tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
             tmem_wait_ld();
@@ -731,6 +788,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
           });
         }
+        ++sc;
       }
     }
   }
