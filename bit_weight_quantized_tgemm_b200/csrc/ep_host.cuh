@@ -63,12 +63,12 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   if (int e = encoder(&enc)) return e;
   for (int i = 0; i < 4; ++i) {
     // the boxes that tiles of up to nt tokens use; a dense call has full tiles and one rest
-    const int lo = i ? 8 << i : 0, hi = 16 << i, rest = c.R % p.nt;
+    const int lo = i ? 8 << i : 0, hi = i < 3 ? 16 << i : kEtTok, rest = c.R % p.nt;
     const bool used = c.offsets ? lo < p.nt : (c.R >= p.nt && p.nt > lo && p.nt <= hi) || (rest > lo && rest <= hi);
     if (!used) continue;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.K) * 2, 128};
-    const cuuint32_t box[3] = {64, 16u << i, 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(et_box_rows(i, p.nt)), 2};
     const cuuint32_t estr[3] = {1, 1, 1};
     if (enc(&tm.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, c.workspace, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

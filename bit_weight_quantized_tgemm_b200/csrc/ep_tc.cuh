@@ -88,7 +88,8 @@ struct EtParams {
 };
 
 // TMA maps.  Activations: the f16 copy as [k block of 64][row][64], boxes of two k blocks
-// (a stage) and 16, 32, 64 or 128 rows, so that one copy brings a tile's stage.
+// (a stage) and 16, 32, 64 or, for larger tiles, nt rows, so that one copy brings a tile's
+// stage.
 struct EtMaps {
   CUtensorMap x[4];
   CUtensorMap w;
@@ -101,8 +102,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// log2 of the box rows / 16 for a tile of mt tokens
-__device__ __forceinline__ int et_box(int mt) { return mt <= 16 ? 0 : mt <= 32 ? 1 : mt <= 64 ? 2 : 3; }
+// the map for a tile of mt tokens, and its box's rows
+__host__ __device__ constexpr int et_box(int mt) { return mt <= 16 ? 0 : mt <= 32 ? 1 : mt <= 64 ? 2 : 3; }
+__host__ __device__ constexpr int et_box_rows(int box, int nt) { return box < 3 ? 16 << box : nt; }
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -364,10 +366,11 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
+        const uint32_t bytes = 256u * et_box_rows(box, p.nt);
         for (int u = 0; u < ksteps; ++u) {
           ok = et_wait(empty_bar(s), ph ^ 1u, abort_flag);
           if (!ok) break;
-          mbar_arrive_expect_tx(full_bar(s), 4096u << box);
+          mbar_arrive_expect_tx(full_bar(s), bytes);
           tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * u);
           ++it;
           if (++s == nx) {
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         const EtTile tl = et_tile(p, tb, t, e);
         const uint32_t ncols = static_cast<uint32_t>((tl.mt + 15) & ~15);
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
-        const uint32_t half = 2048u << et_box(tl.mt);  // bytes of a k block's box
+        const uint32_t half = 128u * et_box_rows(et_box(tl.mt), p.nt);  // bytes of a k block's box
         uint32_t d_tmem = 0;
         for (int u = 0; u < ksteps; ++u) {
           const bool first = u == 0 || (SUMS && u % kSeg == 0);  // of an accumulator segment
@@ -736,39 +739,53 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             if (i < mt) dst[at(i)] = __float2bfloat16_rn(f[i]);
         }
       };
+      const int chunks = (tl.mt + 15) >> 4;
       if constexpr (SUMS) {
-        // 8-token chunks of this set's parity: running sum += a segment, rounded to nearest
-        constexpr int kMine = kEtSumTok / 16;
-        const int chunks = (tl.mt + 7) >> 3;
-        float sum[kMine][8];
+        // running sums of this set's chunks += a segment, rounded to nearest; the whole sums go
+        // back into the last segment's accumulator
+        constexpr int kMine = (kEtSumTok / 16 + 1) / 2;
+        float sum[kMine][16];
 #pragma unroll
         for (int k = 0; k < kMine; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[k][i] = 0.f;
-        for (int u = 0; u < ksteps; u += kSeg, ++sc) {
-          const uint32_t ab = sc & 1u;
+          for (int i = 0; i < 16; ++i) sum[k][i] = 0.f;
+#pragma unroll 1
+        for (int u = 0; u < ksteps; u += kSeg) {
+          const uint32_t ab = sc & 1u, tsrc = t_lane + ab * tmm.acc + 16 * set;
           ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < kMine; ++k) {
             if (2 * k + set >= chunks) break;
-            uint32_t v[8];
-            tmem_ld_32x32b_x8(t_lane + ab * tmm.acc + 8 * (2 * k + set), v);
-            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[k][i] += __uint_as_float(v[i]);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[8];
+              tmem_ld_32x32b_x8(tsrc + 32 * k + 8 * h, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) sum[k][8 * h + i] += __uint_as_float(v[i]);
+            }
           }
-          release(ab);
+          if (u + kSeg < ksteps) {
+            release(ab);
+            ++sc;
+          }
         }
+        const uint32_t tdst = t_lane + (sc & 1u) * tmm.acc + 16 * set;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
           if (2 * k + set >= chunks) break;
-          finish(sum[k], 8 * (2 * k + set), [] {});
+          uint32_t v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[k][i]);
+          tmem_st_32x32b_x16(tdst + 32 * k, v);
         }
-      } else {
-        const int chunks = (tl.mt + 15) >> 4;
+        tmem_wait_st();
+      }
+      {
         const uint32_t ab = sc & 1u;
         auto accumulated = [&] {
+          if (SUMS) return;
           ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
           tc_fence_after();
         };
