@@ -150,7 +150,7 @@ int run_ep(const EpCall& c) {
   if (c.R < 1 || c.x_rows < 1 || c.N < 1 || c.K < kblock || c.K % kblock) return TGEMM_EINVAL;
   if (c.E < 1 || c.E > kEtMaxExperts) return TGEMM_EINVAL;
   if (static_cast<int64_t>(c.E) * c.N > INT32_MAX - kEtRows) return TGEMM_ETOOLARGE;
-  if (c.N > (1 << 27)) return TGEMM_ETOOLARGE;  // 16 rows of y within 32-bit offsets
+  if (c.N > (1 << 24)) return TGEMM_ETOOLARGE;  // a tile of y within 32-bit offsets
   if (!dtype_ok(c.out_dtype)) return TGEMM_EINVAL;
   if (!aligned(c.x, 16) || !aligned(c.wq, 16) || !aligned(c.y, 16)) return TGEMM_EALIGN;
   if (!aligned(c.scales, c.fmt == 0 ? 2 : 4)) return TGEMM_EALIGN;

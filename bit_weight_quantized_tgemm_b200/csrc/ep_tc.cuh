@@ -272,14 +272,14 @@ __device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
 // since f16 weights alone are 2^-12 relative off.
 //
 // SUMS (f32 y): the tensor core adds each K = 16 step to the f32 accumulator with truncation,
-// 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 32 steps the
+// 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 48 steps the
 // epilogue warps take the accumulator into running sums in registers, rounded to nearest.  They
 // hold 80 tokens a tile.
 template <int FMT, bool SPLIT, bool SUMS>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
   using F = EtFmt<FMT>;
-  constexpr int kSeg = SPLIT ? 2 : 4;    // units of an accumulator segment
+  constexpr int kSeg = SPLIT ? 3 : 6;    // units of an accumulator segment
   constexpr int kAU = SPLIT ? 2 : 1;     // A stages of a unit
   static_assert(FMT == 1 || !SPLIT, "ternary weights are exact in f16");
   static_assert(!SPLIT || SUMS, "the low parts are for f32 y");
@@ -656,10 +656,11 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       // for before the next one (13000 cycles a chunk instead of 700).  bf16 outputs leave in
       // pairs: neighbouring lanes trade, so that one has (n, n + 1) of an even token and the
       // other of the odd one.
+      const int64_t tile0 = static_cast<int64_t>(tl.m0) * p.N;
       auto finish = [&](auto& f, int m, auto&& sums) {
         constexpr int kN = sizeof(f) / sizeof(float);
         const int mt = min(kN, tl.mt - m);
-        const int64_t row0 = static_cast<int64_t>(tl.m0 + m) * p.N;
+        const int64_t row0 = tile0 + static_cast<uint32_t>(m) * static_cast<uint32_t>(p.N);
         const int64_t i0 = row0 + (nv ? n : p.N - 1);
         auto at = [&](int i) { return static_cast<uint32_t>(min(i, mt - 1)) * static_cast<uint32_t>(p.N); };
         uint16_t g[kN];
