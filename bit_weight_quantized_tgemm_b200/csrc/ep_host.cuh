@@ -136,12 +136,20 @@ int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
   return c.fmt == 0 ? go(std::integral_constant<int, 0>{}) : go(std::integral_constant<int, 1>{});
 }
 
-// Whether the small path serves a call (see ep_small.cuh); tgemm_set_path overrides it.
-bool ep_is_small(int R, int E, bool grouped) {
+// Whether the small path serves a call; tgemm_set_path overrides it.  Measured in chains of calls
+// (us, small path / tensor path):
+//   dense, ternary   8 tokens  9728 x 2560  8.1 / 12.0;  2560 x 9728 11.2 / 26.4
+//                   16 tokens  9728 x 2560 13.5 / 12.1;  2560 x 9728 18.6 / 26.3;  2560^2 6.6 / 10.9
+//   64 experts 1408 x 2048, ternary: 24 rows 14.4 / 20.3, 192 rows 32.5 / 35.6, 384 rows 41.6 / 36.1
+//   8 experts 4864 x 2560, 4-bit: 32 rows 29.7 / 30.2, 64 rows 39.2 / 32.9
+// Up to 8 tokens the weights meet one MMA tile of tokens.  Up to 16 the tensor path is behind
+// only while its blocks of 128 weight rows leave most SMs idle.
+bool ep_is_small(int R, int E, int N, bool grouped) {
   const int p = g_path.load();
   if (p == TGEMM_PATH_TENSOR) return false;
   if (p != TGEMM_PATH_AUTO) return true;
-  return grouped ? R <= 16 : R <= 16;
+  if (grouped) return R <= 16 || R <= 4 * E;
+  return R <= 8 || (R <= 16 && N < 6144);
 }
 
 int run_ep(const EpCall& c) {
@@ -194,7 +202,7 @@ int run_ep(const EpCall& c) {
       overlaps(c.y, y_bytes, c.offsets, c.offsets ? (static_cast<size_t>(c.E) + 1) * 4 : 0) ||
       overlaps(c.y, y_bytes, c.rows, c.rows ? static_cast<size_t>(c.R) * 4 : 0))
     return TGEMM_EINVAL;
-  const bool small = ep_is_small(c.R, c.E, c.offsets != nullptr);
+  const bool small = ep_is_small(c.R, c.E, c.N, c.offsets != nullptr);
   const size_t need = small ? 0 : ep_ws_bytes(c.R, c.K);
   if (need && (!c.workspace || c.ws_bytes < need)) return TGEMM_EWORKSPACE;
   if (need && !aligned(c.workspace, 256)) return TGEMM_EALIGN;

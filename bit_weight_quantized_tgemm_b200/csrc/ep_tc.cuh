@@ -240,6 +240,19 @@ __device__ __forceinline__ uint32_t hfma2_u32(uint32_t a, uint32_t b, uint32_t c
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// 4-bit weights for a bf16 y: f16(q s - f16(z s)), pairs as q4_word_to_f16; zs2 = f16(z s) twice.
+// Two roundings, as f16(f16(q - z) s) has, for one f16 instruction a pair less (these take 2
+// cycles a warp, and 256 of them a unit are what the dequantizers need at least).
+__device__ __forceinline__ void q4_word_scaled(uint32_t w, uint32_t s2, uint32_t zs2, uint32_t* o) {
+  constexpr uint32_t kMagic[2] = {0x64006400u, 0x54005400u};  // 1024, 64
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = i & 1;
+    const uint32_t q = hsub2_u32(lop3_and_or(i < 2 ? w : (w >> 8), 0x000F000Fu << (4 * j), kMagic[j]), kMagic[j]);
+    o[i] = hfma2_u32(q, s2, zs2 ^ 0x80008000u);
+  }
+}
+
 // 4-bit weights w = (q - z) s as a high and a low f16 part, pairs as q4_word_to_f16: with
 // t = f16(q - z), hi = f16(t s) and lo = f16(t s - hi), which one fma gives.  EXACT: q - z is an
 // f16 value for every code; otherwise its rounding error (two-sum), times s, joins lo.
@@ -593,9 +606,9 @@ __global__ void __launch_bounds__(kEtThreads, 1)
 #pragma unroll
               for (int j = 0; j < 4; ++j) q2_word_to_f16(wd[j], s2, o + 8 * j);
             } else {
-              const uint32_t z2 = (s1 >> 16) | (s1 & 0xFFFF0000u);
+              const uint32_t zs2 = hmul2_u32((s1 >> 16) | (s1 & 0xFFFF0000u), s2);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) q4_word_to_f16(wd[j], s2, z2, o + 4 * j);
+              for (int j = 0; j < 4; ++j) q4_word_scaled(wd[j], s2, zs2, o + 4 * j);
             }
             if (k == 0) slot_wait();
             if constexpr (kRegs == 32)

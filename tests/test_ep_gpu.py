@@ -32,7 +32,7 @@ def run(fmt, M, N, K, act, ep, out, seed=0, x_scale=1.0, **kw):
     assert got is y
     torch.cuda.synchronize()
     assert canary_intact(buf, M * N)
-    check(y, *reference(fmt, x, w, e["bias"], act, e["gate"], e["residual"], out == "f32"),
+    check(y, *reference(fmt, x, w, e["bias"], act, e["gate"], e["residual"], out == "f32", sc),
           f"{fmt} {M}x{N}x{K} {act} {ep} {out}")
 
 

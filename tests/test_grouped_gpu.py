@@ -42,7 +42,7 @@ def run(fmt, counts, N, K, act="none", ep="", out="bf16", gather=None, first=0, 
             xs = x[sl] if rows is None else x[rows[sl].long()]
             check(y[sl], *reference(fmt, xs, w[i], None if e["bias"] is None else e["bias"][i], act,
                                     None if e["gate"] is None else e["gate"][sl],
-                                    None if e["residual"] is None else e["residual"][sl], out == "f32"),
+                                    None if e["residual"] is None else e["residual"][sl], out == "f32", sc[i]),
                   f"{fmt} expert {i} of {counts}")
         at += n
     assert (y[:first] == 77).all() and (y[at:] == 77).all(), "rows of no expert were written"
