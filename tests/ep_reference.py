@@ -2,10 +2,11 @@
 
 The error bound of one output follows the steps of the computation.  With S = sum_k |w x|:
   product   bf16 activations are exact in f16 down to 2^-14, below that off by at most 2^-25
-            each; ternary weights are exact in f16; 4-bit weights are f16(q s - f16(z s)) when y
-            is bf16, two roundings of half a step, 2^-11 of |w| (2^-25 where it is subnormal)
-            and 2^-11 of |z s|, and are a high and a low f16 part (error of the low part's
-            rounding 2^-22, and 2^-25 absolute where it is subnormal) when y is f32; the f32 sum over k is at most K / 16 + 16
+            each; ternary weights are exact in f16; 4-bit weights take two f16 roundings of half a
+            step when y is bf16, f16(q s - f16(z s)) or f16(f16(q - z) s): 2^-11 of |w| and 2^-11
+            of |z s| or |w|, so at most 2^-11 (2 |w| + |z s|) (2^-25 each where subnormal); they
+            are a high and a low f16 part (error of the low part's rounding 2^-22, and 2^-25
+            absolute where it is subnormal) when y is f32; the f32 sum over k is at most K / 16 + 16
             accumulations, each off by at most a whole step 2^-23 of S
   bias      one f32 rounding
   act       slope at most 1.13 for the four activations; its own steps at most 8 f32 steps of
@@ -71,7 +72,7 @@ def reference(fmt, x, w, bias, act, gate, residual, out_f32, sc=None):
             dv = dv + 2.0 ** -22 * S + 2.0 ** -25 * ax
         else:
             zs = (sc[..., 0].double() * sc[..., 1].double()).abs().repeat_interleave(64, -1)
-            dv = dv + 2.0 ** -11 * (S + x.abs() @ zs.T) + 2 * 2.0 ** -25 * ax
+            dv = dv + 2.0 ** -11 * (2 * S + x.abs() @ zs.T) + 2 * 2.0 ** -25 * ax
     v = x @ w.T
     if bias is not None:
         v = v + bias.double()

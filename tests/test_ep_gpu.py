@@ -69,6 +69,26 @@ def test_every_epilogue(M, act, ep, out):
     run("q2", M, 136, 256, act, ep, out, seed=5)
 
 
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("M,N,K", [(2600, 3500, 256), (2305, 4099, 128), (1281, 9300, 384)])
+@pytest.mark.parametrize("act,ep", [("gelu_tanh", "bias:bf16"), ("none", "bias:f32 gate:row"), ("silu", "gate:full"),
+                                    ("none", "residual:f32"), ("gelu", "bias:bf16 gate:full residual:bf16")])
+def test_many_tiles(fmt, M, N, K, act, ep):
+    """Several tiles for each SM, ragged in both directions, odd widths (no pairs of outputs)."""
+    run(fmt, M, N, K, act, ep, "bf16", seed=N)
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+def test_many_tiles_with_the_smallest_workspace(fmt):
+    M, N, K = 2600, 3500, 256
+    wq, sc, w = pack(fmt, (N, K), 3, "cuda")
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    ws = torch.empty(M * K * 2, dtype=torch.uint8, device="cuda")
+    y = fn(fmt)(x, wq, sc, act=tg.ACT_RELU, workspace=ws)
+    torch.cuda.synchronize()
+    check(y, *reference(fmt, x, w, None, "relu", None, None, False, sc), fmt)
+
+
 @pytest.mark.parametrize("M", [4, 70])
 @pytest.mark.parametrize("fmt", ["q2", "q4"])
 def test_large_and_small_activations(M, fmt):
