@@ -11,6 +11,19 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && x < y + nb && y < x + na;
 }
 
+// Let a kernel use `bytes` of dynamic shared memory, once per device (`done`: a bit for each).
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TGEMM_ECUDA;
+  const uint64_t bit = uint64_t{1} << dev;
+  if (done.load(std::memory_order_acquire) & bit) return TGEMM_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return TGEMM_ECUDA;
+  done.fetch_or(bit, std::memory_order_release);
+  return TGEMM_OK;
+}
+static_assert(kMaxDevices <= 64, "a bit for each device");
+
 struct EpCall {
   int fmt;
   const uint16_t* x;
@@ -51,13 +64,8 @@ int et_pick_nt(int M, int tiles_n, int most, int sms) {
 
 template <int FMT, bool SPLIT, bool SUMS>
 int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(ep_tc_kernel<FMT, SPLIT, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               EtFmt<FMT>::kSmemBytes);
-  });
-  if (err != cudaSuccess) return TGEMM_ECUDA;
+  static std::atomic<uint64_t> done{0};
+  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS>, EtFmt<FMT>::kSmemBytes, done)) return e;
   EtMaps tm;
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (int e = encoder(&enc)) return e;
@@ -93,12 +101,8 @@ int64_t max_chunks(int R, int E, int nt) {
 template <int FMT, int T>
 int launch_ep_small(EsParams p, int64_t chunks, int sms, cudaStream_t st) {
   constexpr int kMost = 225 * 1024, kHalf = 112 * 1024;  // one CTA or two on an SM
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(ep_small_kernel<FMT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-  });
-  if (err != cudaSuccess) return TGEMM_ECUDA;
+  static std::atomic<uint64_t> done{0};
+  if (int e = allow_smem(ep_small_kernel<FMT, T>, kMost, done)) return e;
   p.tiles_n = (p.N + kEsRows - 1) / kEsRows;
   const int64_t items = chunks * p.tiles_n;
   if (items > INT32_MAX / 2) return TGEMM_ETOOLARGE;
@@ -136,6 +140,11 @@ int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
   return c.fmt == 0 ? go(std::integral_constant<int, 0>{}) : go(std::integral_constant<int, 1>{});
 }
 
+constexpr int kEsMaxK = 32768;  // a warp's scales of K fit in shared memory
+static_assert(es_smem_bytes(0, 2, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024 &&
+                  es_smem_bytes(1, 2, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024,
+              "shared memory of the small path");
+
 // Whether the small path serves a call; tgemm_set_path overrides it.  Measured in chains of calls
 // (us, small path / tensor path):
 //   dense, ternary   8 tokens  9728 x 2560  8.1 / 12.0;  2560 x 9728 11.2 / 26.4
@@ -144,8 +153,9 @@ int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
 //   8 experts 4864 x 2560, 4-bit: 32 rows 29.7 / 30.2, 64 rows 39.2 / 32.9
 // Up to 8 tokens the weights meet one MMA tile of tokens.  Up to 16 the tensor path is behind
 // only while its blocks of 128 weight rows leave most SMs idle.
-bool ep_is_small(int R, int E, int N, bool grouped) {
+bool ep_is_small(int R, int E, int N, int K, bool grouped) {
   const int p = g_path.load();
+  if (K > kEsMaxK) return false;
   if (p == TGEMM_PATH_TENSOR) return false;
   if (p != TGEMM_PATH_AUTO) return true;
   if (grouped) return R <= 16 || R <= 4 * E;
@@ -202,7 +212,7 @@ int run_ep(const EpCall& c) {
       overlaps(c.y, y_bytes, c.offsets, c.offsets ? (static_cast<size_t>(c.E) + 1) * 4 : 0) ||
       overlaps(c.y, y_bytes, c.rows, c.rows ? static_cast<size_t>(c.R) * 4 : 0))
     return TGEMM_EINVAL;
-  const bool small = ep_is_small(c.R, c.E, c.N, c.offsets != nullptr);
+  const bool small = ep_is_small(c.R, c.E, c.N, c.K, c.offsets != nullptr);
   const size_t need = small ? 0 : ep_ws_bytes(c.R, c.K);
   if (need && (!c.workspace || c.ws_bytes < need)) return TGEMM_EWORKSPACE;
   if (need && !aligned(c.workspace, 256)) return TGEMM_EALIGN;
@@ -276,13 +286,8 @@ int run_sort(const int* ids, int T, int k, int E, int* offsets, int* rows, int* 
   if (need && !aligned(workspace, 256)) return TGEMM_EALIGN;
   DeviceInfo di;
   if (int e = current_device_info(&di)) return e;
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (kSortWarps + 2) * kEtMaxExperts * 4);
-  });
-  if (err != cudaSuccess) return TGEMM_ECUDA;
+  static std::atomic<uint64_t> done{0};
+  if (int e = allow_smem(sort_place_kernel, (kSortWarps + 2) * kEtMaxExperts * 4, done)) return e;
   const cudaStream_t st = as_stream(stream);
   const int G = sort_grid(n, E);
   SortParams p;

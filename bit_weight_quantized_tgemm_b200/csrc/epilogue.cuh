@@ -17,16 +17,28 @@ struct EpArgs {
   int bias_f32, gate_rows, residual_f32, out_f32, act;
 };
 
-// v / (1 + exp(-t)).  The quotient is within 2 f32 steps; a denominator past 2^126 gives 0,
-// as v * 2^-126 would round to for any v of use.
-__device__ __forceinline__ float ep_logistic(float v, float t) { return __fdividef(v, 1.f + expf(-t)); }
+__device__ __forceinline__ float ep_exp2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+// v / (1 + 2^-t), from the exponential and quotient units: the exponential is within 2^-22 and the
+// quotient within 2 f32 steps, and a denominator past 2^126 gives 0, as v * 2^-126 would round
+// to for any v of use.
+// 1536 x 9472 x 1280 ternary with a tanh GELU: 56 us with expf, 50 us.
+__device__ __forceinline__ float ep_logistic(float v, float t) { return __fdividef(v, 1.f + ep_exp2(-t)); }
+
+constexpr float kLog2E = 1.4426950408889634f;
 
 template <int ACT>
 __device__ __forceinline__ float ep_act(float v) {
-  if (ACT == kActSilu) return ep_logistic(v, v);
+  if (ACT == kActSilu) return ep_logistic(v, kLog2E * v);
   if (ACT == kActGelu) return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-  // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)),  2 u = 2 sqrt(2 / pi) (v + 0.044715 v^3)
-  if (ACT == kActGeluTanh) return ep_logistic(v, 1.5957691216057308f * fmaf(0.044715f * v * v, v, v));
+  // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2 u)),  2 u = 2 sqrt(2 / pi) v (1 + 0.044715 v^2)
+  if (ACT == kActGeluTanh) {
+    constexpr float kC = 1.5957691216057308f * kLog2E;
+    return ep_logistic(v, v * fmaf(0.044715f * kC, v * v, kC));
+  }
   if (ACT == kActRelu) return v < 0.f ? 0.f : v;  // keeps a NaN
   return v;
 }

@@ -1073,13 +1073,13 @@ int tgemm_q4(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, void* y, 
 
 size_t tgemm_ep_workspace_size(int op, int M, int N, int K) {
   if (M < 1 || N < 1 || K < 1 || (op != TGEMM_OP_Q2 && op != TGEMM_OP_Q4)) return 0;
-  return ep_is_small(M, 1, N, false) ? 0 : ep_ws_bytes(M, K);
+  return ep_is_small(M, 1, N, K, false) ? 0 : ep_ws_bytes(M, K);
 }
 
 size_t tgemm_grouped_workspace_size(int op, int R, int E, int N, int K) {
   if (R < 1 || E < 1 || E > TGEMM_MAX_EXPERTS || N < 1 || K < 1 || (op != TGEMM_OP_Q2 && op != TGEMM_OP_Q4))
     return 0;
-  return ep_is_small(R, E, N, true) ? 0 : ep_ws_bytes(R, K);
+  return ep_is_small(R, E, N, K, true) ? 0 : ep_ws_bytes(R, K);
 }
 
 int tgemm_q2_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* d, const tgemm_epilogue* ep, void* y, int M,

@@ -105,6 +105,45 @@ def test_zero_points_of_any_size(M, out):
     run("q4", M, 72, 512, "none", "", out, z_lo=0.0)
 
 
+@pytest.mark.parametrize("M", [3, 50])
+@pytest.mark.parametrize("N,K", [(70, 256), (40, 384), (130, 1024)])
+def test_scales_on_any_16_bit_address(M, N, K):
+    """Ternary scales that start between two words, with rows of an even and an odd number."""
+    wq, sc, w = pack("q2", (N, K), 12, "cuda")
+    d = torch.empty(N * K // 128 + 1, dtype=torch.float16, device="cuda")[1:].view(N, K // 128)
+    d.copy_(sc)
+    assert d.data_ptr() % 4 == 2
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    y = tg.gemm_q2_ep(x, wq, d, out_dtype=tg.OUT_F32)
+    torch.cuda.synchronize()
+    assert torch.equal(y, tg.gemm_q2_ep(x, wq, sc, out_dtype=tg.OUT_F32))
+    check(y, *reference("q2", x, w, None, "none", None, None, True), "shifted scales")
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("K", [20480, 32768, 33792])
+def test_very_long_rows(fmt, K):
+    """Longer than the small path keeps activations for, and than it takes at all."""
+    run(fmt, 3, 40, K, "none", "bias:f32", "f32")
+    run(fmt, 13, 40, K, "none", "", "bf16")
+
+
+@pytest.mark.parametrize("fmt", ["q2", "q4"])
+@pytest.mark.parametrize("M", [3, 50])
+def test_large_scales(fmt, M):
+    """Scales up to f16's range, where the offsets of the unpacked codes must not overflow."""
+    N, K = 72, 256
+    wq, sc, w = pack(fmt, (N, K), 2, "cuda")
+    big = 2.0 ** 11
+    s2, w2 = sc.clone(), w * big
+    (s2 if fmt == "q2" else s2[..., 0]).mul_(big)
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    for out in ("f32", "bf16"):
+        y = fn(fmt)(x, wq, s2, out_dtype=tg.OUT_F32 if out == "f32" else tg.OUT_BF16)
+        torch.cuda.synchronize()
+        check(y, *reference(fmt, x, w2, None, "none", None, None, out == "f32", s2), f"{fmt} {M} {out}")
+
+
 @pytest.mark.parametrize("M", [3, 50, 260])
 @pytest.mark.parametrize("out", [tg.OUT_F32, tg.OUT_BF16])
 def test_in_place_on_the_residual(M, out):
