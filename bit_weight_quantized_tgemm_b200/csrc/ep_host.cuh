@@ -239,7 +239,10 @@ int run_ep(const EpCall& c) {
   p.R = c.R;
   p.tiles_n = (c.N + kEtRows - 1) / kEtRows;
   const int most = out_f32 ? kEtSumTok : kEtTok;  // tokens of a tile
-  p.nt = c.offsets ? most : et_pick_nt(c.R, p.tiles_n, most, di.sms);
+  // Grouped: room for twice an expert's rows on average, of which 32 or 64 leave shared memory for
+  // more weights on their way (an expert with more rows takes more tiles).
+  const int64_t twice = 2 * static_cast<int64_t>(c.R) / c.E;
+  p.nt = !c.offsets ? et_pick_nt(c.R, p.tiles_n, most, di.sms) : twice <= 32 ? 32 : twice <= 64 ? 64 : most;
   p.ksteps = (c.K + kEtBK - 1) / kEtBK;
   p.nblocks = c.K / (c.fmt == 0 ? 128 : 64);
   p.offsets = c.offsets;

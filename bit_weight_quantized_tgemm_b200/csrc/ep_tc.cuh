@@ -24,8 +24,8 @@ constexpr int kEtScaleWarp = 3;
 constexpr int kEtDeqWarp0 = 4;
 constexpr int kEtEpiWarp0 = kEtDeqWarp0 + 4 * kEtGroups;
 constexpr int kEtThreads = (kEtEpiWarp0 + 8) * 32;
-constexpr int kEtXRing = 5 * kEtTok * 256;      // activation ring: 5 slots of 128 tokens or 10 of 64
-constexpr int kEtXSlots = 10;
+constexpr int kEtRing = 192 * 1024;             // activation slots, then weight stages
+constexpr int kEtXSlots = 10, kEtWStages = 16;  // the most of each
 constexpr int kEtChunk = 16;                    // scale blocks of a chunk
 constexpr int kEtScBufs = 3;                    // chunks of scales in shared memory
 constexpr int kEtMaxExperts = 1024;
@@ -33,8 +33,17 @@ constexpr int kEtMaxExperts = 1024;
 struct EtTmem {
   int acc, a0, na;  // columns of an accumulator, first A column, A stages
 };
-// activation slots
-__host__ __device__ constexpr int et_nx(int nt) { return nt <= kEtTok / 2 ? 10 : 5; }
+// Activation slots, and tokens of a slot.  Large tiles need the activations' depth (32 KB a unit
+// at 64 bytes a cycle); small ones need many weights on their way from memory.
+__host__ __device__ constexpr int et_nx(int nt) { return nt <= 32 ? 10 : nt <= 64 ? 8 : 5; }
+__host__ __device__ constexpr int et_slot_tok(int nt) { return nt <= 32 ? 32 : nt <= 64 ? 64 : kEtTok; }
+// weight stages of wbytes each
+__host__ __device__ constexpr int et_nw(int nt, int wbytes) {
+  return (kEtRing - et_nx(nt) * et_slot_tok(nt) * 256) / wbytes < kEtWStages
+             ? (kEtRing - et_nx(nt) * et_slot_tok(nt) * 256) / wbytes : kEtWStages;
+}
+static_assert(et_nw(128, 8192) == 4 && et_nw(64, 8192) == 8 && et_nw(32, 8192) == 14 && et_nw(128, 4096) == 8,
+              "weight stages");
 // The A stages hold no more units than there are activation slots: a dequant group reports unit
 // i on its slot's barrier once it may write its A stages, that is when the unit that had them
 // before is multiplied, and the barrier must then be done with unit i - slots.
@@ -58,19 +67,17 @@ static_assert(et_tmem_fits(false, false, 16) && et_tmem_fits(false, false, 64) &
 template <int FMT>
 struct EtFmt {
   static constexpr int kWqRowBytes = FMT == 0 ? 32 : 64;
-  static constexpr int kWStages = FMT == 0 ? 8 : 4;
   static constexpr int kWBytes = kEtRows * kWqRowBytes;
   static constexpr int kXOff = 0;
-  static constexpr int kWOff = kEtXRing;
   // A chunk's scales as 32-bit words [word][row] (Q2: two blocks' d, 4-bit: a block's (s, z)):
   // the pitch keeps the scale warp's writes and the dequantizers' reads free of bank conflicts.
   static constexpr int kScWords = FMT == 0 ? kEtChunk / 2 : kEtChunk;
   static constexpr int kScPitch = 4 * kEtRows + (FMT == 0 ? 16 : 8);
   static constexpr int kScBytes = kScWords * kScPitch;
-  static constexpr int kScOff = kWOff + kWStages * kWBytes;
+  static constexpr int kScOff = kEtRing;
   static constexpr int kTabOff = kScOff + kEtScBufs * kScBytes;
   static constexpr int kBarOff = kTabOff + 2 * (kEtMaxExperts + 2) * 4;
-  static constexpr int kNumBars = 2 * kEtXSlots + 2 * kWStages + 4 + 1 + 2 * kEtScBufs;
+  static constexpr int kNumBars = 2 * kEtXSlots + 2 * kEtWStages + 4 + 1 + 2 * kEtScBufs;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -305,8 +312,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kEtXSlots + s); };
   auto wfull_bar = [&](uint32_t w) { return bar0 + 8u * (2 * kEtXSlots + w); };
-  auto wempty_bar = [&](uint32_t w) { return bar0 + 8u * (2 * kEtXSlots + F::kWStages + w); };
-  constexpr uint32_t kBar1 = 2 * kEtXSlots + 2 * F::kWStages;
+  auto wempty_bar = [&](uint32_t w) { return bar0 + 8u * (2 * kEtXSlots + kEtWStages + w); };
+  constexpr uint32_t kBar1 = 2 * kEtXSlots + 2 * kEtWStages;
   auto accfull_bar = [&](uint32_t a) { return bar0 + 8u * (kBar1 + a); };
   auto accempty_bar = [&](uint32_t a) { return bar0 + 8u * (kBar1 + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (kBar1 + 4);
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       mbar_init(full_bar(s), 1 + 4);  // the producer's expect_tx + a dequant group
       mbar_init(empty_bar(s), 1);     // MMA commit
     }
-    for (int w = 0; w < F::kWStages; ++w) {
+    for (int w = 0; w < kEtWStages; ++w) {
       mbar_init(wfull_bar(w), 1);
       mbar_init(wempty_bar(w), 4);
     }
@@ -367,7 +374,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
   const EtTmem tmm = et_tmem(SPLIT, SUMS, p.nt);
   // activation slots: unit i uses slot i % nx, for the (i / nx)-th time
-  const uint32_t nx = et_nx(p.nt), xslot = kEtXRing / nx;
+  const uint32_t nx = et_nx(p.nt), xslot = et_slot_tok(p.nt) * 256;
+  const uint32_t nw = et_nw(p.nt, F::kWBytes), w_ring = sbase + nx * xslot;  // weight stages
 
   // Every role walks the same stream of units: tile by tile, unit by unit along k.
   if (warp == 0) {
@@ -446,23 +454,25 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   } else if (warp == kEtWProdWarp) {
     // ------------------------------------------------------------ packed-weight producer
     if (elect_one()) {
-      uint32_t it = 0;
+      uint32_t it = 0, w = 0, ph = 0;
       int e = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int row = tl.e * p.N + tl.n0;
-        for (int u = 0; u < ksteps; ++u, ++it) {
-          const uint32_t w = it % F::kWStages;
-          ok = et_wait(wempty_bar(w), ((it / F::kWStages) & 1u) ^ 1u, abort_flag);
+        for (int u = 0; u < ksteps; ++u) {
+          ok = et_wait(wempty_bar(w), ph ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(wfull_bar(w), F::kWBytes);
-          tma_load_2d(sbase + F::kWOff + w * F::kWBytes, &tm.w, wfull_bar(w),
-                      u * F::kWqRowBytes, row);
+          tma_load_2d(w_ring + w * F::kWBytes, &tm.w, wfull_bar(w), u * F::kWqRowBytes, row);
+          ++it;
+          if (++w == nw) {
+            w = 0;
+            ph ^= 1u;
+          }
         }
       }
-      for (uint32_t j = (it > F::kWStages ? it - F::kWStages : 0); j < it; ++j)
-        mbar_wait_drain(wfull_bar(j % F::kWStages), (j / F::kWStages) & 1u);
+      for (uint32_t j = (it > nw ? it - nw : 0); j < it; ++j) mbar_wait_drain(wfull_bar(j % nw), (j / nw) & 1u);
     }
   } else if (warp == kEtScaleWarp) {
     // ------------------------------------------------------------ scales -> shared memory
@@ -523,7 +533,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const int grp = (warp - kEtDeqWarp0) >> 2;
     const int rt = 32 * q + lane;                  // weight row within the tile
     const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + tmm.a0;
-    const uint32_t w_mine = sbase + F::kWOff + rt * F::kWqRowBytes;
+    const uint32_t w_mine = w_ring + rt * F::kWqRowBytes;
     const uint8_t* s_mine = smem + F::kScOff + 4 * rt;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
     const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
@@ -532,6 +542,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     int mine = grp, as = grp * kAU % tmm.na;  // the group's next unit, from the chunk's first; its A stage
     uint32_t i0 = 0, cidx = 0;        // the chunk's first unit; chunks
     uint32_t xs = grp;                // the unit's activation slot
+    uint32_t w = grp, wph = 0;        // its weight stage, and that one's phase
     // the last unit that had the unit's A stages before is `back` units earlier; jr: its place
     // in two rounds of the activation slots
     const uint32_t back = (tmm.na - (kAU - 1)) / kAU;
@@ -564,7 +575,6 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           if (jr >= 2 * nx) jr -= 2 * nx;
         };
         {
-          const uint32_t w = i % F::kWStages;
           constexpr int kChunks = F::kWqRowBytes / 16;      // 16 bytes of codes each
           constexpr int kRegs = FMT == 0 ? 32 : 16;         // f16 pairs of a chunk
           const uint32_t src = w_mine + w * F::kWBytes;
@@ -577,7 +587,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * mine + 1) * F::kScPitch);
           }
           const bool exact = SPLIT && __all_sync(0xFFFFFFFFu, q4_zero_exact(sc[0] >> 16) && q4_zero_exact(sc[FMT == 0 ? 0 : 1] >> 16));
-          ok = et_wait_warp(wfull_bar(w), (i / F::kWStages) & 1u, abort_flag) && ok;
+          ok = et_wait_warp(wfull_bar(w), wph, abort_flag) && ok;
           uint4 cw[kChunks];
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) cw[k] = ld_shared_v4(src + ((k ^ swz) << 4));
@@ -585,6 +595,11 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(wempty_bar(w));
+          w += kEtGroups;
+          if (w >= nw) {
+            w -= nw;
+            wph ^= 1u;
+          }
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
             const uint32_t wd[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
