@@ -25,44 +25,28 @@ constexpr int kEtDeqWarp0 = 4;
 constexpr int kEtEpiWarp0 = kEtDeqWarp0 + 4 * kEtGroups;
 constexpr int kEtThreads = (kEtEpiWarp0 + 8) * 32;
 constexpr int kEtRing = 192 * 1024;             // activation slots, then weight stages
-constexpr int kEtXSlots = 10, kEtWStages = 16;  // the most of each
+constexpr int kEtXSlots = 8, kEtWStages = 16;   // the most of each
 constexpr int kEtChunk = 16;                    // scale blocks of a chunk
 constexpr int kEtScBufs = 3;                    // chunks of scales in shared memory
 constexpr int kEtMaxExperts = 1024;
-// Tensor memory: two accumulators and from column `a0` the A stages (64 columns each).
-struct EtTmem {
-  int acc, a0, na;  // columns of an accumulator, first A column, A stages
-};
-// Activation slots, and tokens of a slot.  Large tiles need the activations' depth (32 KB a unit
-// at 64 bytes a cycle); small ones need many weights on their way from memory.
-__host__ __device__ constexpr int et_nx(int nt) { return nt <= 32 ? 10 : nt <= 64 ? 8 : 5; }
+// Every ring has a power of two of places, so that place and phase of unit i come from its bits.
+// Activation slots hold 32, 64 or 128 tokens.  Large tiles bring 32 KB of activations a unit; with
+// small ones many weights are to be on their way from memory.
 __host__ __device__ constexpr int et_slot_tok(int nt) { return nt <= 32 ? 32 : nt <= 64 ? 64 : kEtTok; }
-// weight stages of wbytes each
-__host__ __device__ constexpr int et_nw(int nt, int wbytes) {
-  return (kEtRing - et_nx(nt) * et_slot_tok(nt) * 256) / wbytes < kEtWStages
-             ? (kEtRing - et_nx(nt) * et_slot_tok(nt) * 256) / wbytes : kEtWStages;
+__host__ __device__ constexpr int et_lx(int nt) { return nt <= 64 ? 3 : 2; }  // log2 of the slots
+// log2 of the weight stages of wbytes each, in the rest of the ring
+__host__ __device__ constexpr int et_lw(int nt, int wbytes) {
+  const int n = (kEtRing - (et_slot_tok(nt) * 256 << et_lx(nt))) / wbytes;
+  return n >= 16 ? 4 : n >= 8 ? 3 : 2;
 }
-static_assert(et_nw(128, 8192) == 4 && et_nw(64, 8192) == 8 && et_nw(32, 8192) == 14 && et_nw(128, 4096) == 8,
+static_assert(et_lw(128, 8192) == 3 && et_lw(64, 8192) == 3 && et_lw(32, 8192) == 4 && et_lw(128, 4096) == 4,
               "weight stages");
+// Tensor memory: two accumulators and from column 256 four A stages of 64 columns.
 // The A stages hold no more units than there are activation slots: a dequant group reports unit
 // i on its slot's barrier once it may write its A stages, that is when the unit that had them
 // before is multiplied, and the barrier must then be done with unit i - slots.
-__host__ __device__ constexpr EtTmem et_tmem(bool split, bool sums, int nt) {
-  return split ? EtTmem{kEtSumTok, 160, 5}  // two stages a unit
-         : sums ? EtTmem{kEtSumTok, 160, 5}
-         : nt <= 64 ? EtTmem{64, 128, 6} : EtTmem{128, 256, 4};
-}
-constexpr bool et_tmem_fits(bool split, bool sums, int nt) {
-  return et_tmem(split, sums, nt).a0 + 64 * et_tmem(split, sums, nt).na <= 512 &&
-         2 * et_tmem(split, sums, nt).acc <= et_tmem(split, sums, nt).a0 &&
-         nt <= et_tmem(split, sums, nt).acc &&
-         et_tmem(split, sums, nt).na / (split ? 2 : 1) <= et_nx(nt);
-}
-static_assert(et_tmem_fits(false, false, 16) && et_tmem_fits(false, false, 64) && et_tmem_fits(false, false, 80) &&
-                  et_tmem_fits(false, false, 128) && et_tmem_fits(false, true, 16) && et_tmem_fits(false, true, 64) &&
-                  et_tmem_fits(false, true, 80) && et_tmem_fits(true, true, 16) && et_tmem_fits(true, true, 64) &&
-                  et_tmem_fits(true, true, 80),
-              "tensor memory, and units in flight");
+constexpr int kEtLA = 2;  // log2 of the A stages
+static_assert(2 * kEtTok <= 256 && 256 + (64 << kEtLA) <= 512 && 2 * kEtSumTok <= 256 && kEtLA <= et_lx(128), "TMEM");
 
 template <int FMT>
 struct EtFmt {
@@ -372,43 +356,39 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const EtTable tb{tab_off, tab_tp};
   const int num_tiles = tab_tp[p.E] * p.tiles_n;
   const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
-  const EtTmem tmm = et_tmem(SPLIT, SUMS, p.nt);
-  // activation slots: unit i uses slot i % nx, for the (i / nx)-th time
-  const uint32_t nx = et_nx(p.nt), xslot = et_slot_tok(p.nt) * 256;
-  const uint32_t nw = et_nw(p.nt, F::kWBytes), w_ring = sbase + nx * xslot;  // weight stages
+  constexpr int kAcc = SUMS ? kEtSumTok : kEtTok, kA0 = 2 * kEtTok;  // an accumulator's columns, the first A column
+  // activation slots and weight stages
+  const int lx = et_lx(p.nt), lw = et_lw(p.nt, F::kWBytes);
+  const uint32_t nx = 1u << lx, xslot = et_slot_tok(p.nt) * 256;
+  const uint32_t nw = 1u << lw, w_ring = sbase + nx * xslot;
 
   // Every role walks the same stream of units: tile by tile, unit by unit along k.
   if (warp == 0) {
     // ------------------------------------------------------------ activation producer
     if (elect_one()) {
-      uint32_t it = 0, s = 0, ph = 0;
+      uint32_t it = 0;
       int e = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
         const uint32_t bytes = 256u * et_box_rows(box, p.nt);
-        for (int u = 0; u < ksteps; ++u) {
-          ok = et_wait(empty_bar(s), ph ^ 1u, abort_flag);
+        for (int u = 0; u < ksteps; ++u, ++it) {
+          const uint32_t s = it & (nx - 1);
+          ok = et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(full_bar(s), bytes);
           tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * u);
-          ++it;
-          if (++s == nx) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
       }
       // every load issued must land before the CTA may exit
       for (uint32_t j = (it > nx ? it - nx : 0); j < it; ++j)
-        mbar_wait_drain(full_bar(j % nx), (j / nx) & 1u);
+        mbar_wait_drain(full_bar(j & (nx - 1)), (j >> lx) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (elect_one()) {
-      uint32_t s = 0, ph = 0, sc = 0;  // activation slot and its phase, accumulator segments
-      int as = 0;               // A stage
+      uint32_t it = 0, sc = 0;  // units, accumulator segments
       int e = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
@@ -417,34 +397,30 @@ __global__ void __launch_bounds__(kEtThreads, 1)
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
         const uint32_t half = 128u * et_box_rows(et_box(tl.mt), p.nt);  // bytes of a k block's box
         uint32_t d_tmem = 0;
-        for (int u = 0; u < ksteps; ++u) {
+        for (int u = 0; u < ksteps; ++u, ++it) {
           const bool first = u == 0 || (SUMS && u % kSeg == 0);  // of an accumulator segment
           if (first) {
             if (SUMS && u > 0) mma_commit(accfull_bar(sc++ & 1u));
             ok = et_wait(accempty_bar(sc & 1u), ((sc >> 1) & 1u) ^ 1u, abort_flag);
             if (!ok) break;
-            d_tmem = tmem_base + (sc & 1u) * tmm.acc;
+            d_tmem = tmem_base + (sc & 1u) * kAcc;
           }
+          const uint32_t s = it & (nx - 1);
           const uint32_t xs = sbase + F::kXOff + s * xslot;
           const uint64_t b0 = smem_desc_sw128(xs);
           const uint64_t b1 = smem_desc_sw128(xs + half);
-          ok = et_wait(full_bar(s), ph, abort_flag);
+          ok = et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int part = 0; part < kAU; ++part) {
-            const uint32_t a_tmem = tmem_base + tmm.a0 + as * 64;
-            if (++as == tmm.na) as = 0;
+            const uint32_t a_tmem = tmem_base + kA0 + (((kAU * it + part) & ((1u << kEtLA) - 1)) * 64);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
                          (part > 0 || kk > 0 || !first) ? 1u : 0u);
           }
           mma_commit(empty_bar(s));
-          if (++s == nx) {
-            s = 0;
-            ph ^= 1u;
-          }
         }
         if (ok) mma_commit(accfull_bar(sc++ & 1u));
       }
@@ -454,25 +430,21 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   } else if (warp == kEtWProdWarp) {
     // ------------------------------------------------------------ packed-weight producer
     if (elect_one()) {
-      uint32_t it = 0, w = 0, ph = 0;
+      uint32_t it = 0;
       int e = 0;
       bool ok = true;
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int row = tl.e * p.N + tl.n0;
-        for (int u = 0; u < ksteps; ++u) {
-          ok = et_wait(wempty_bar(w), ph ^ 1u, abort_flag);
+        for (int u = 0; u < ksteps; ++u, ++it) {
+          const uint32_t w = it & (nw - 1);
+          ok = et_wait(wempty_bar(w), ((it >> lw) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(wfull_bar(w), F::kWBytes);
           tma_load_2d(w_ring + w * F::kWBytes, &tm.w, wfull_bar(w), u * F::kWqRowBytes, row);
-          ++it;
-          if (++w == nw) {
-            w = 0;
-            ph ^= 1u;
-          }
         }
       }
-      for (uint32_t j = (it > nw ? it - nw : 0); j < it; ++j) mbar_wait_drain(wfull_bar(j % nw), (j / nw) & 1u);
+      for (uint32_t j = (it > nw ? it - nw : 0); j < it; ++j) mbar_wait_drain(wfull_bar(j & (nw - 1)), (j >> lw) & 1u);
     }
   } else if (warp == kEtScaleWarp) {
     // ------------------------------------------------------------ scales -> shared memory
@@ -532,47 +504,31 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const int q = warp & 3;                        // TMEM lane quarter
     const int grp = (warp - kEtDeqWarp0) >> 2;
     const int rt = 32 * q + lane;                  // weight row within the tile
-    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + tmm.a0;
+    const uint32_t a_lane = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + kA0;
     const uint32_t w_mine = w_ring + rt * F::kWqRowBytes;
     const uint8_t* s_mine = smem + F::kScOff + 4 * rt;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
     const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
     const int my_tiles = num_tiles > static_cast<int>(blockIdx.x)
                              ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
-    int mine = grp, as = grp * kAU % tmm.na;  // the group's next unit, from the chunk's first; its A stage
-    uint32_t i0 = 0, cidx = 0;        // the chunk's first unit; chunks
-    uint32_t xs = grp;                // the unit's activation slot
-    uint32_t w = grp, wph = 0;        // its weight stage, and that one's phase
-    // the last unit that had the unit's A stages before is `back` units earlier; jr: its place
-    // in two rounds of the activation slots
-    const uint32_t back = (tmm.na - (kAU - 1)) / kAU;
-    uint32_t jr = grp + 2 * nx - back;
-    if (jr >= 2 * nx) jr -= 2 * nx;
+    uint32_t i = grp, i0 = 0, cidx = 0;  // the group's next unit; the chunk's first; chunks
     bool ok = true;
     for (int t = 0; t < my_tiles; ++t)
     for (int c = 0; c < nchunks; ++c, ++cidx) {
-      const int nu = min(kCU, ksteps - c * kCU);
+      const uint32_t i1 = i0 + min(kCU, ksteps - c * kCU);
       const uint32_t sb = cidx % kEtScBufs;
       const uint8_t* s_chunk = s_mine + sb * F::kScBytes;
       // also when none of the units is ours: the release below must not run ahead of the fill
       ok = et_wait_warp(sfull_bar(sb), (cidx / kEtScBufs) & 1u, abort_flag) && ok;
-      for (; mine < nu; mine += kEtGroups) {
-        const uint32_t i = i0 + mine;
-        uint32_t a_dst[kAU];
-#pragma unroll
-        for (int part = 0; part < kAU; ++part) {
-          const int sl = as + part;
-          a_dst[part] = a_lane + (sl >= tmm.na ? sl - tmm.na : sl) * 64;
-        }
-        as += kEtGroups * kAU;
-        while (as >= tmm.na) as -= tmm.na;
-        // the unit's A stages are free once the units that had them before are multiplied
+      for (; i < i1; i += kEtGroups) {
+        const uint32_t m = i - i0, w = i & (nw - 1);
+        const uint32_t a_dst = a_lane + ((kAU * i) & ((1u << kEtLA) - 1)) * 64;
+        // the unit's A stages are free once the unit that had them before is multiplied
         auto slot_wait = [&]() {
-          if (i >= back)
-            ok = et_wait_warp(empty_bar(jr >= nx ? jr - nx : jr), jr >= nx ? 1u : 0u, abort_flag) && ok;
+          constexpr uint32_t kBack = (1u << kEtLA) / kAU;
+          const uint32_t j = i - kBack;
+          if (i >= kBack) ok = et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag) && ok;
           tc_fence_after();
-          jr += kEtGroups;
-          if (jr >= 2 * nx) jr -= 2 * nx;
         };
         {
           constexpr int kChunks = F::kWqRowBytes / 16;      // 16 bytes of codes each
@@ -580,14 +536,14 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           const uint32_t src = w_mine + w * F::kWBytes;
           uint32_t sc[FMT == 0 ? 1 : 2];
           if (FMT == 0) {
-            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + (mine >> 1) * F::kScPitch);
-            sc[0] = mine & 1 ? sc[0] >> 16 : sc[0] & 0xFFFFu;
+            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + (m >> 1) * F::kScPitch);
+            sc[0] = m & 1 ? sc[0] >> 16 : sc[0] & 0xFFFFu;
           } else {
-            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * mine * F::kScPitch);
-            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * mine + 1) * F::kScPitch);
+            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * m * F::kScPitch);
+            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * m + 1) * F::kScPitch);
           }
           const bool exact = SPLIT && __all_sync(0xFFFFFFFFu, q4_zero_exact(sc[0] >> 16) && q4_zero_exact(sc[FMT == 0 ? 0 : 1] >> 16));
-          ok = et_wait_warp(wfull_bar(w), wph, abort_flag) && ok;
+          ok = et_wait_warp(wfull_bar(w), (i >> lw) & 1u, abort_flag) && ok;
           uint4 cw[kChunks];
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) cw[k] = ld_shared_v4(src + ((k ^ swz) << 4));
@@ -595,11 +551,6 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(wempty_bar(w));
-          w += kEtGroups;
-          if (w >= nw) {
-            w -= nw;
-            wph ^= 1u;
-          }
 #pragma unroll
           for (int k = 0; k < kChunks; ++k) {
             const uint32_t wd[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
@@ -627,23 +578,20 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             }
             if (k == 0) slot_wait();
             if constexpr (kRegs == 32)
-              tmem_st_32x32b_x32(a_dst[0] + 32 * k, o);
+              tmem_st_32x32b_x32(a_dst + 32 * k, o);
             else
-              tmem_st_32x32b_x16(a_dst[0] + 16 * k, o);
-            if constexpr (SPLIT) tmem_st_32x32b_x16(a_dst[kAU - 1] + 16 * k, lo);
+              tmem_st_32x32b_x16(a_dst + 16 * k, o);
+            if constexpr (SPLIT) tmem_st_32x32b_x16(a_dst + 64 + 16 * k, lo);
           }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(full_bar(xs));
-        xs += kEtGroups;
-        if (xs >= nx) xs -= nx;
+        if (lane == 0 && ok) mbar_arrive(full_bar(i & (nx - 1)));
       }
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(sempty_bar(sb));
-      mine -= nu;
-      i0 += nu;
+      i0 = i1;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -780,7 +728,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           for (int i = 0; i < 16; ++i) sum[k][i] = 0.f;
 #pragma unroll 1
         for (int u = 0; u < ksteps; u += kSeg) {
-          const uint32_t ab = sc & 1u, tsrc = t_lane + ab * tmm.acc + 16 * set;
+          const uint32_t ab = sc & 1u, tsrc = t_lane + ab * kAcc + 16 * set;
           ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
           tc_fence_after();
 #pragma unroll
@@ -800,7 +748,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             ++sc;
           }
         }
-        const uint32_t tdst = t_lane + (sc & 1u) * tmm.acc + 16 * set;
+        const uint32_t tdst = t_lane + (sc & 1u) * kAcc + 16 * set;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
           if (2 * k + set >= chunks) break;
@@ -827,7 +775,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           finish(f, 16 * cc, [&] {
             if (cc == set) accumulated();  // the first chunk's operands are on their way already
             uint32_t v[16];
-            tmem_ld_32x32b_x16(t_lane + ab * tmm.acc + 16 * cc, v);
+            tmem_ld_32x32b_x16(t_lane + ab * kAcc + 16 * cc, v);
             tmem_wait_ld();
             if (cc + 2 >= chunks) release(ab);  // the accumulator is read out
 #pragma unroll
