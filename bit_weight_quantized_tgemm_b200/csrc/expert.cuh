@@ -18,9 +18,11 @@ struct SortParams {
   int* offsets;  // [E + 1]
   int* rows;     // [n] source token of each sorted row, -1 behind the last
   int* pos;      // [n] sorted row of each pair, -1 for an id outside [0, E)
-  int* hist;     // [G][E] pairs of each CTA by expert (G > 1)
+  int* hist;     // [G][sort_pitch(E)] pairs of each CTA by expert (G > 1)
   int n, k, E, run;  // run: pairs per warp
 };
+
+__host__ __device__ constexpr int sort_pitch(int E) { return (E + 3) & ~3; }
 
 __device__ __forceinline__ void sort_run_bounds(const SortParams& p, int cta, int warp, int& lo, int& hi) {
   const int64_t a = (static_cast<int64_t>(cta) * kSortWarps + warp) * p.run;
@@ -41,10 +43,25 @@ __device__ __forceinline__ void sort_load(const SortParams& p, int i0, int hi, i
     if (id[j] < 0 || id[j] >= p.E) id[j] = -1;
 }
 
+// The lanes with this lane's expert, for each of four batches: a vote on each bit of the ids (a
+// match of the ids takes some 200 cycles a warp, one vote and its two instructions 10).  `bits`
+// holds E, so that -1 is no expert.
+__device__ __forceinline__ void sort_peers(const int (&id)[4], int bits, uint32_t (&same)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) same[j] = 0xFFFFFFFFu;
+  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t one = (static_cast<uint32_t>(id[j]) >> b) & 1u;
+      same[j] &= __ballot_sync(0xFFFFFFFFu, one) ^ (one - 1u);
+    }
+  }
+}
+
 // Pairs of each CTA by expert.
 __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(const SortParams p) {
   extern __shared__ int st_cnt[];  // [E]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) st_cnt[e] = 0;
   __syncthreads();
   pdl_trigger_and_wait();
@@ -54,15 +71,13 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_count_kernel(const SortP
     int id[4];
     sort_load(p, i0, hi, id);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i0 + 32 * j >= hi) break;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
-      if (id[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(st_cnt + id[j], __popc(same));
-    }
+    for (int j = 0; j < 4; ++j)
+      if (id[j] >= 0) atomicAdd(st_cnt + id[j], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-    p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = st_cnt[e];
+  const int pitch = sort_pitch(p.E);
+  for (int e = threadIdx.x; e < pitch; e += blockDim.x)
+    p.hist[static_cast<int64_t>(blockIdx.x) * pitch + e] = e < p.E ? st_cnt[e] : 0;
 }
 
 // Places the CTA's pairs.  With one CTA (G = 1) it needs no counts from before.
@@ -77,42 +92,48 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
   __syncthreads();
   pdl_trigger_and_wait();
   if (G > 1) {
-    // every CTA's counts: thread (seg, e) adds up every nseg-th CTA's; the order does not
-    // matter, they are whole numbers
-    const int ep = (p.E + 31) & ~31, nseg = static_cast<int>(blockDim.x) / ep;
-    const int seg = tid / ep, e = tid - seg * ep;
-    if (seg < nseg && e < p.E) {
-      int sum = 0, before = 0;
-#pragma unroll 8
+    // every CTA's counts: thread (seg, e4) adds up every nseg-th CTA's for four experts; the
+    // order does not matter, they are whole numbers
+    const int quads = sort_pitch(p.E) / 4, nseg = static_cast<int>(blockDim.x) / quads;
+    const int seg = tid / quads, e4 = 4 * (tid - seg * quads);
+    if (seg < nseg) {
+      int sum[4] = {0, 0, 0, 0}, before[4] = {0, 0, 0, 0};
+#pragma unroll 4
       for (int c = seg; c < G; c += nseg) {
-        const int v = __ldg(p.hist + static_cast<int64_t>(c) * p.E + e);
-        sum += v;
-        if (c < g) before += v;
+        const int4 q = __ldg(reinterpret_cast<const int4*>(p.hist + static_cast<int64_t>(c) * sort_pitch(p.E) + e4));
+        const int v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[i] += v[i];
+          if (c < g) before[i] += v[i];
+        }
       }
-      atomicAdd(s_total + e, sum);
-      atomicAdd(s_before + e, before);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e4 + i < p.E) {
+          atomicAdd(s_total + e4 + i, sum[i]);
+          if (before[i]) atomicAdd(s_before + e4 + i, before[i]);
+        }
     }
   }
   int lo, hi;
   sort_run_bounds(p, g, warp, lo, hi);
-  int* base = st_base + warp * p.E;  // the warp's own counters: no atomics
+  int* base = st_base + warp * p.E;  // the warp's own counters
   for (int i0 = lo; i0 < hi; i0 += 128) {
     int id[4];
     sort_load(p, i0, hi, id);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i0 + 32 * j >= hi) break;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
-      if (id[j] >= 0 && lane == __ffs(same) - 1) base[id[j]] += __popc(same);
-      __syncwarp();
-    }
+    for (int j = 0; j < 4; ++j)
+      if (id[j] >= 0) atomicAdd(base + id[j], 1);
   }
   __syncthreads();
   // E <= blockDim.x: thread e owns expert e
-  int mine = 0;
+  int mine = 0, cnt[kSortWarps];
   if (tid < p.E) {
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) mine += st_base[w * p.E + tid];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) cnt[w] = st_base[w * p.E + tid];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) mine += cnt[w];
   }
   const int total = tid < p.E ? (G > 1 ? s_total[tid] : mine) : 0;
   int incl = total;
@@ -136,31 +157,32 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
   if (warp > 0) incl += part[warp - 1];
   if (tid < p.E) {
     int at = incl - total + s_before[tid];
-#pragma unroll 8
+#pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const int v = st_base[w * p.E + tid];
       st_base[w * p.E + tid] = at;
-      at += v;
+      at += cnt[w];
     }
     if (g == 0) {
       p.offsets[tid] = incl - total;
       if (tid == p.E - 1) p.offsets[p.E] = incl;
     }
   }
+  const int bits = 32 - __clz(p.E);
   const int kept = part[kSortWarps - 1];
   __syncthreads();
   for (int i0 = lo; i0 < hi; i0 += 128) {
     int id[4];
     sort_load(p, i0, hi, id);
+    uint32_t same[4];
+    sort_peers(id, bits, same);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (i0 + 32 * j >= hi) break;
       const int i = i0 + 32 * j + lane;
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, id[j]);
       int at = -1;
-      if (id[j] >= 0) at = base[id[j]] + __popc(same & ((1u << lane) - 1u));
+      if (id[j] >= 0) at = base[id[j]] + __popc(same[j] & ((1u << lane) - 1u));
       __syncwarp();
-      if (id[j] >= 0 && lane == __ffs(same) - 1) base[id[j]] += __popc(same);
+      if (id[j] >= 0 && lane == __ffs(same[j]) - 1) base[id[j]] += __popc(same[j]);
       __syncwarp();
       if (i < hi) {
         p.pos[i] = at;
