@@ -64,8 +64,9 @@ int et_pick_nt(int M, int tiles_n, int most, int sms) {
 
 template <int FMT, bool SPLIT, bool SUMS>
 int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) {
+  using F = EtFmt<FMT, SPLIT>;
   static std::atomic<uint64_t> done{0};
-  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS>, EtFmt<FMT>::kSmemBytes, done)) return e;
+  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS>, F::kSmemBytes, done)) return e;
   EtMaps tm;
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (int e = encoder(&enc)) return e;
@@ -76,7 +77,7 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
     if (!used) continue;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.K) * 2, 128};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(et_box_rows(i, p.nt)), 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(et_box_rows(i, p.nt)), F::kBK / 64};
     const cuuint32_t estr[3] = {1, 1, 1};
     if (enc(&tm.x[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, c.workspace, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -85,11 +86,11 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
   }
   const uint64_t row_bytes = static_cast<uint64_t>(c.K) / (FMT == 0 ? 4 : 2);
   if (int e = make_map_2d(&tm.w, c.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row_bytes,
-                          static_cast<uint64_t>(c.E) * c.N, EtFmt<FMT>::kWqRowBytes, kEtRows,
-                          FMT == 0 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B))
+                          static_cast<uint64_t>(c.E) * c.N, F::kWqRowBytes, kEtRows,
+                          F::kWSwizzle))
     return e;
   return launch(FMT == 0 ? TGEMM_KIND_TC_Q2 : TGEMM_KIND_TC_Q4, st, [&] {
-    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, EtFmt<FMT>::kSmemBytes, st, tm, p);
+    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, F::kSmemBytes, st, tm, p);
   });
 }
 
@@ -243,7 +244,7 @@ int run_ep(const EpCall& c) {
   // more weights on their way (an expert with more rows takes more tiles).
   const int64_t twice = 2 * static_cast<int64_t>(c.R) / c.E;
   p.nt = !c.offsets ? et_pick_nt(c.R, p.tiles_n, most, di.sms) : twice <= 32 ? 32 : twice <= 64 ? 64 : most;
-  p.ksteps = (c.K + kEtBK - 1) / kEtBK;
+  p.ksteps = split ? c.K / 64 : (c.K + 127) / 128;
   p.nblocks = c.K / (c.fmt == 0 ? 128 : 64);
   p.offsets = c.offsets;
   p.scales = c.scales;

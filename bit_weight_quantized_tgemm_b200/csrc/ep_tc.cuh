@@ -17,7 +17,6 @@ namespace tgemm {
 constexpr int kEtRows = 128;
 constexpr int kEtTok = 128;
 constexpr int kEtSumTok = 80;                   // most tokens of a tile with running sums
-constexpr int kEtBK = 128;
 constexpr int kEtGroups = 3;                    // dequant groups of 4 warps, stages in turn
 constexpr int kEtWProdWarp = 2;
 constexpr int kEtScaleWarp = 3;
@@ -33,26 +32,31 @@ constexpr int kEtMaxExperts = 1024;
 // Activation slots hold 32, 64 or 128 tokens.  Large tiles bring 32 KB of activations a unit; with
 // small ones many weights are to be on their way from memory.
 __host__ __device__ constexpr int et_slot_tok(int nt) { return nt <= 32 ? 32 : nt <= 64 ? 64 : kEtTok; }
-__host__ __device__ constexpr int et_lx(int nt) { return nt <= 64 ? 3 : 2; }  // log2 of the slots
+// log2 of the slots, for units of bk
+__host__ __device__ constexpr int et_lx(int nt, int bk) { return nt * bk <= 64 * 128 || bk < 128 ? 3 : 2; }
 // log2 of the weight stages of wbytes each, in the rest of the ring
-__host__ __device__ constexpr int et_lw(int nt, int wbytes) {
-  const int n = (kEtRing - (et_slot_tok(nt) * 256 << et_lx(nt))) / wbytes;
+__host__ __device__ constexpr int et_lw(int nt, int bk, int wbytes) {
+  const int n = (kEtRing - (et_slot_tok(nt) * bk * 2 << et_lx(nt, bk))) / wbytes;
   return n >= 16 ? 4 : n >= 8 ? 3 : 2;
 }
-static_assert(et_lw(128, 8192) == 3 && et_lw(64, 8192) == 3 && et_lw(32, 8192) == 4 && et_lw(128, 4096) == 4,
+static_assert(et_lw(128, 128, 8192) == 3 && et_lw(64, 128, 8192) == 3 && et_lw(32, 128, 8192) == 4 &&
+                  et_lw(128, 128, 4096) == 4 && et_lw(128, 64, 4096) == 4,
               "weight stages");
 // Tensor memory: two accumulators and from column 256 four A stages of 64 columns.
 // The A stages hold no more units than there are activation slots: a dequant group reports unit
 // i on its slot's barrier once it may write its A stages, that is when the unit that had them
 // before is multiplied, and the barrier must then be done with unit i - slots.
 constexpr int kEtLA = 2;  // log2 of the A stages
-static_assert(2 * kEtTok <= 256 && 256 + (64 << kEtLA) <= 512 && 2 * kEtSumTok <= 256 && kEtLA <= et_lx(128), "TMEM");
+static_assert(2 * kEtTok <= 256 && 256 + (64 << kEtLA) <= 512 && 2 * kEtSumTok <= 256 && kEtLA <= et_lx(128, 128), "TMEM");
 
-template <int FMT>
+template <int FMT, bool SPLIT>
 struct EtFmt {
-  static constexpr int kWqRowBytes = FMT == 0 ? 32 : 64;
+  // k of a unit.  With two f16 parts a weight, 64: an A stage then holds both, and four units
+  // instead of two are between the dequantizers and the tensor core.
+  static constexpr int kBK = SPLIT ? 64 : 128;
+  static constexpr int kWqRowBytes = FMT == 0 ? kBK / 4 : kBK / 2;
+  static constexpr CUtensorMapSwizzle kWSwizzle = kWqRowBytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B;
   static constexpr int kWBytes = kEtRows * kWqRowBytes;
-  static constexpr int kXOff = 0;
   // A chunk's scales as 32-bit words [word][row] (Q2: two blocks' d, 4-bit: a block's (s, z)):
   // the pitch keeps the scale warp's writes and the dequantizers' reads free of bank conflicts.
   static constexpr int kScWords = FMT == 0 ? kEtChunk / 2 : kEtChunk;
@@ -71,16 +75,15 @@ struct EtParams {
   int N, K, E, R;
   int nt;                 // tokens per tile, a multiple of 16
   int tiles_n;            // ceil(N / 128)
-  int ksteps;             // units (128 k) of a tile: ceil(K / 128)
+  int ksteps;             // units of a tile: K / kBK, rounded up
   int nblocks;            // scale blocks of a row: K / 128 or K / 64
   const int* offsets;     // [E + 1] row ranges, or null: one expert, rows [0, R)
   const uint16_t* scales;
   EpArgs ep;
 };
 
-// TMA maps.  Activations: the f16 copy as [k block of 64][row][64], boxes of two k blocks
-// (a stage) and 16, 32, 64 or, for larger tiles, nt rows, so that one copy brings a tile's
-// stage.
+// TMA maps.  Activations: the f16 copy as [k block of 64][row][64], boxes of a unit's one or two
+// k blocks and 16, 32, 64 or, for larger tiles, nt rows, so that one copy brings a tile's unit.
 struct EtMaps {
   CUtensorMap x[4];
   CUtensorMap w;
@@ -282,12 +285,11 @@ __device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
 template <int FMT, bool SPLIT, bool SUMS>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
-  using F = EtFmt<FMT>;
-  constexpr int kSeg = SPLIT ? 3 : 6;    // units of an accumulator segment
-  constexpr int kAU = SPLIT ? 2 : 1;     // A stages of a unit
+  using F = EtFmt<FMT, SPLIT>;
+  constexpr int kSeg = 6;  // units (of 8 steps) of an accumulator segment
   static_assert(FMT == 1 || !SPLIT, "ternary weights are exact in f16");
   static_assert(!SPLIT || SUMS, "the low parts are for f32 y");
-  constexpr int kCU = FMT == 0 ? 16 : 8;  // units of a chunk of scales
+  constexpr int kCU = FMT == 1 && !SPLIT ? 8 : 16;  // units of a chunk of scales
   extern __shared__ uint8_t et_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(et_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -358,8 +360,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
   constexpr int kAcc = SUMS ? kEtSumTok : kEtTok, kA0 = 2 * kEtTok;  // an accumulator's columns, the first A column
   // activation slots and weight stages
-  const int lx = et_lx(p.nt), lw = et_lw(p.nt, F::kWBytes);
-  const uint32_t nx = 1u << lx, xslot = et_slot_tok(p.nt) * 256;
+  const int lx = et_lx(p.nt, F::kBK), lw = et_lw(p.nt, F::kBK, F::kWBytes);
+  const uint32_t nx = 1u << lx, xslot = et_slot_tok(p.nt) * F::kBK * 2;
   const uint32_t nw = 1u << lw, w_ring = sbase + nx * xslot;
 
   // Every role walks the same stream of units: tile by tile, unit by unit along k.
@@ -372,13 +374,13 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
-        const uint32_t bytes = 256u * et_box_rows(box, p.nt);
+        const uint32_t bytes = 2u * F::kBK * et_box_rows(box, p.nt);
         for (int u = 0; u < ksteps; ++u, ++it) {
           const uint32_t s = it & (nx - 1);
           ok = et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(full_bar(s), bytes);
-          tma_load_3d(sbase + F::kXOff + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, 2 * u);
+          tma_load_3d(sbase + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, u * (F::kBK / 64));
         }
       }
       // every load issued must land before the CTA may exit
@@ -406,20 +408,17 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             d_tmem = tmem_base + (sc & 1u) * kAcc;
           }
           const uint32_t s = it & (nx - 1);
-          const uint32_t xs = sbase + F::kXOff + s * xslot;
+          const uint32_t xs = sbase + s * xslot;
           const uint64_t b0 = smem_desc_sw128(xs);
-          const uint64_t b1 = smem_desc_sw128(xs + half);
+          const uint64_t b1 = SPLIT ? b0 : smem_desc_sw128(xs + half);  // SPLIT: the low parts meet the same x
           ok = et_wait(full_bar(s), (it >> lx) & 1u, abort_flag);
           if (!ok) break;
           tc_fence_after();
+          const uint32_t a_tmem = tmem_base + kA0 + (it & ((1u << kEtLA) - 1)) * 64;
 #pragma unroll
-          for (int part = 0; part < kAU; ++part) {
-            const uint32_t a_tmem = tmem_base + kA0 + (((kAU * it + part) & ((1u << kEtLA) - 1)) * 64);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
-                         (part > 0 || kk > 0 || !first) ? 1u : 0u);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(d_tmem, a_tmem + 8u * kk, (kk < 4 ? b0 : b1) + 2u * (kk & 3), idesc,
+                       (kk > 0 || !first) ? 1u : 0u);
           mma_commit(empty_bar(s));
         }
         if (ok) mma_commit(accfull_bar(sc++ & 1u));
@@ -500,7 +499,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   } else if (warp < kEtEpiWarp0) {
     // ------------------------------------------------------------ dequantizers
     // Group grp takes every third unit of the stream; each of its threads unpacks one weight
-    // row's 128 codes of the unit.
+    // row's codes of the unit.
     const int q = warp & 3;                        // TMEM lane quarter
     const int grp = (warp - kEtDeqWarp0) >> 2;
     const int rt = 32 * q + lane;                  // weight row within the tile
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const uint32_t w_mine = w_ring + rt * F::kWqRowBytes;
     const uint8_t* s_mine = smem + F::kScOff + 4 * rt;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
-    const uint32_t swz = FMT == 0 ? (rt >> 2) & 1 : (rt >> 1) & 3;
+    const uint32_t swz = F::kWqRowBytes == 32 ? (rt >> 2) & 1 : (rt >> 1) & 3;
     const int my_tiles = num_tiles > static_cast<int>(blockIdx.x)
                              ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
     uint32_t i = grp, i0 = 0, cidx = 0;  // the group's next unit; the chunk's first; chunks
@@ -522,10 +521,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       ok = et_wait_warp(sfull_bar(sb), (cidx / kEtScBufs) & 1u, abort_flag) && ok;
       for (; i < i1; i += kEtGroups) {
         const uint32_t m = i - i0, w = i & (nw - 1);
-        const uint32_t a_dst = a_lane + ((kAU * i) & ((1u << kEtLA) - 1)) * 64;
-        // the unit's A stages are free once the unit that had them before is multiplied
+        const uint32_t a_dst = a_lane + (i & ((1u << kEtLA) - 1)) * 64;
+        // the unit's A stage is free once the unit that had it before is multiplied
         auto slot_wait = [&]() {
-          constexpr uint32_t kBack = (1u << kEtLA) / kAU;
+          constexpr uint32_t kBack = 1u << kEtLA;
           const uint32_t j = i - kBack;
           if (i >= kBack) ok = et_wait_warp(empty_bar(j & (nx - 1)), (j >> lx) & 1u, abort_flag) && ok;
           tc_fence_after();
@@ -534,15 +533,16 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           constexpr int kChunks = F::kWqRowBytes / 16;      // 16 bytes of codes each
           constexpr int kRegs = FMT == 0 ? 32 : 16;         // f16 pairs of a chunk
           const uint32_t src = w_mine + w * F::kWBytes;
-          uint32_t sc[FMT == 0 ? 1 : 2];
+          constexpr int kSc = FMT == 1 && !SPLIT ? 2 : 1;   // scale words
+          uint32_t sc[kSc];
           if (FMT == 0) {
             sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + (m >> 1) * F::kScPitch);
             sc[0] = m & 1 ? sc[0] >> 16 : sc[0] & 0xFFFFu;
           } else {
-            sc[0] = *reinterpret_cast<const uint32_t*>(s_chunk + 2 * m * F::kScPitch);
-            sc[FMT] = *reinterpret_cast<const uint32_t*>(s_chunk + (2 * m + 1) * F::kScPitch);
+#pragma unroll
+            for (int k = 0; k < kSc; ++k) sc[k] = *reinterpret_cast<const uint32_t*>(s_chunk + (kSc * m + k) * F::kScPitch);
           }
-          const bool exact = SPLIT && __all_sync(0xFFFFFFFFu, q4_zero_exact(sc[0] >> 16) && q4_zero_exact(sc[FMT == 0 ? 0 : 1] >> 16));
+          const bool exact = SPLIT && __all_sync(0xFFFFFFFFu, q4_zero_exact(sc[0] >> 16));
           ok = et_wait_warp(wfull_bar(w), (i >> lw) & 1u, abort_flag) && ok;
           uint4 cw[kChunks];
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           for (int k = 0; k < kChunks; ++k) {
             const uint32_t wd[4] = {cw[k].x, cw[k].y, cw[k].z, cw[k].w};
             uint32_t o[kRegs];
-            const uint32_t s1 = sc[FMT == 0 ? 0 : k >> 1];
+            const uint32_t s1 = sc[kSc == 1 ? 0 : k >> 1];
             const uint32_t s2 = (s1 & 0xFFFFu) | (s1 << 16);
             uint32_t lo[SPLIT ? kRegs : 1];
             (void)lo;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
               tmem_st_32x32b_x32(a_dst + 32 * k, o);
             else
               tmem_st_32x32b_x16(a_dst + 16 * k, o);
-            if constexpr (SPLIT) tmem_st_32x32b_x16(a_dst + 64 + 16 * k, lo);
+            if constexpr (SPLIT) tmem_st_32x32b_x16(a_dst + 32 + 16 * k, lo);
           }
         }
         tmem_wait_st();
