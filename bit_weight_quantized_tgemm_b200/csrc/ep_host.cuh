@@ -45,28 +45,105 @@ bool dtype_ok(int dt) { return dt == TGEMM_OUT_F32 || dt == TGEMM_OUT_BF16; }
 // Workspace of the tensor-core path: the f16 copy of the activations.
 size_t ep_ws_bytes(int R, int K) { return round_up(static_cast<size_t>(R) * K * 2, 256); }
 
-// Tokens per tile of a dense call: the candidate whose fullest CTA has the least to do.  A
-// 128-k stage costs 4 cycles per token on the tensor core and no less than the dequantizers
-// need for its 128 x 128 weights.
-int et_pick_nt(int M, int tiles_n, int most, int sms) {
-  int best = most;
+// The most row chunks of `nt` that R rows in E groups can make (one group: exactly those).
+int64_t max_chunks(int R, int E, int nt) {
+  return (R + static_cast<int64_t>(std::min(R, E)) * (nt - 1)) / nt;
+}
+
+// Tokens per tile and CTAs per tile of a dense call: the pair whose fullest CTA has the least to
+// do.  A unit costs 4 cycles per token on the tensor core, and no less than 350, which the
+// dequantizers need (0.27 us in all).  Few tiles leave SMs idle, so that clusters of up to 8 CTAs
+// share the units of one.  Meeting costs them 2 to 3 us and more with each; another 2 us where the
+// clusters nearly fill the device, since one starts when an SM is free for each of its CTAs.
+// Measured (us, chains of calls, by CTAs a tile):
+//   17 x 2560 x 9728 ternary, 20 tiles: 1 27.3, 2 19.8, 3 16.5, 4 15.0, 5 14.5, 6 14.3
+//   17 x 2560 x 2560 ternary, 20 tiles: 1 11.1, 2 10.5, 3 9.9, 4 9.6, 5 9.7, 6 10.0
+//   256 x 1408 x 2048 ternary, 44 tiles (of 45 clusters of 3): 1 11.5, 2 11.8, 3 14.4
+//   17 x 2560 x 9728 4-bit, f32 y, 20 tiles: 1 51.5, 2 31.7, 3 25.1, 4 21.4, 5 19.7, 6 18.8
+struct EtPlan {
+  int nt, split;
+};
+template <typename Held>  // held(s): clusters of s CTAs that the device runs at once
+EtPlan et_plan(int M, int tiles_n, int units, int most, int sms, Held&& held) {
+  EtPlan best{most, 1};
   int64_t best_cost = INT64_MAX;
   for (int nt = 16; nt <= most; nt += 16) {
     const int64_t tiles = static_cast<int64_t>((M + nt - 1) / nt) * tiles_n;
-    const int64_t cost = (tiles + sms - 1) / sms * std::max(4 * nt, 350);
+    const int64_t unit = std::max(4 * nt, 350);
+    const int64_t cost = (tiles + sms - 1) / sms * units * unit;
     if (cost <= best_cost) {
       best_cost = cost;
-      best = nt;
+      best = {nt, 1};
+    }
+    for (int s = 2; s <= kEtMaxSplit && tiles * s <= sms && 4 * s <= units; ++s) {
+      int64_t c = static_cast<int64_t>((units + 2 * s - 1) / (2 * s)) * 2 * unit + 3600 + 400 * (s - 2);
+      if (c >= best_cost) continue;
+      const int64_t n = held(s);
+      if (5 * tiles > 4 * n) c += 2600;
+      if (c < best_cost && tiles <= n) {
+        best_cost = c;
+        best = {nt, s};
+      }
     }
   }
   return best;
 }
 
 template <int FMT, bool SPLIT, bool SUMS>
-int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) {
+int launch_ep_tc(const EpCall& c, EtParams p, int sms, cudaStream_t st) {
   using F = EtFmt<FMT, SPLIT>;
   static std::atomic<uint64_t> done{0};
-  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS>, F::kSmemBytes, done)) return e;
+  static std::atomic<uint64_t> done_share{0};
+  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS, false>, F::kSmemBytes, done)) return e;
+  if (int e = allow_smem(ep_tc_kernel<FMT, SPLIT, SUMS, true>, F::kSmemBytes, done_share)) return e;
+  p.ksteps = (c.K + F::kBK - 1) / F::kBK;
+  constexpr int kMost = SUMS ? kEtSumTok : kEtTok;  // tokens of a tile
+  p.split = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {1, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = kEtThreads;
+  cfg.dynamicSmemBytes = F::kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  if (c.offsets) {
+    // Room for twice an expert's rows on average, of which 32 or 64 leave shared memory for more
+    // weights on their way (an expert with more rows takes more tiles).
+    const int64_t twice = 2 * static_cast<int64_t>(c.R) / c.E;
+    p.nt = twice <= 32 ? 32 : twice <= 64 ? 64 : kMost;
+  } else {
+    // clusters of s that the current device holds at once, asked once (0: not yet)
+    static std::atomic<int> held[kMaxDevices][kEtMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TGEMM_ECUDA;
+    const EtPlan plan = et_plan(c.R, p.tiles_n, p.ksteps, kMost, sms, [&](int s) {
+      int n = held[dev][s].load(std::memory_order_relaxed);
+      if (n == 0) {
+        cudaLaunchConfig_t q = cfg;
+        q.gridDim = s * sms;
+        attr[1].val.clusterDim.x = s;
+        q.attrs = attr + 1;
+        q.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, ep_tc_kernel<FMT, SPLIT, SUMS, true>, &q) != cudaSuccess || n < 1) {
+          cudaGetLastError();
+          n = -1;
+        }
+        held[dev][s].store(n, std::memory_order_relaxed);
+      }
+      return n;
+    });
+    p.nt = plan.nt;
+    p.split = plan.split;
+  }
+  // the most tiles there can be: an expert with rows has at most one partly filled tile
+  const int64_t tiles = max_chunks(c.R, c.E, p.nt) * p.tiles_n;
+  if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
+  cfg.gridDim = static_cast<unsigned>(p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, sms));
   EtMaps tm;
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (int e = encoder(&enc)) return e;
@@ -90,13 +167,9 @@ int launch_ep_tc(const EpCall& c, const EtParams& p, int grid, cudaStream_t st) 
                           F::kWSwizzle))
     return e;
   return launch(FMT == 0 ? TGEMM_KIND_TC_Q2 : TGEMM_KIND_TC_Q4, st, [&] {
-    return pdl_launch(ep_tc_kernel<FMT, SPLIT, SUMS>, grid, kEtThreads, F::kSmemBytes, st, tm, p);
+    return p.split > 1 ? cudaLaunchKernelEx(&cfg, ep_tc_kernel<FMT, SPLIT, SUMS, true>, tm, p)
+                       : cudaLaunchKernelEx(&cfg, ep_tc_kernel<FMT, SPLIT, SUMS, false>, tm, p);
   });
-}
-
-// The most row chunks of `nt` that R rows in E groups can make.
-int64_t max_chunks(int R, int E, int nt) {
-  return std::min<int64_t>(R, static_cast<int64_t>(R) / nt + std::min(R, E));
 }
 
 template <int FMT, int T>
@@ -148,19 +221,21 @@ static_assert(es_smem_bytes(0, 2, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts
 
 // Whether the small path serves a call; tgemm_set_path overrides it.  Measured in chains of calls
 // (us, small path / tensor path):
-//   dense, ternary   8 tokens  9728 x 2560  8.1 / 12.0;  2560 x 9728 11.2 / 26.4
-//                   16 tokens  9728 x 2560 13.5 / 12.1;  2560 x 9728 18.6 / 26.3;  2560^2 6.6 / 10.9
+//   dense, ternary   8 tokens  9728 x 2560  8.1 / 11.7;  2560 x 9728 10.4 / 14.2;  4-bit 16.0 / 15.4
+//                   16 tokens  1408 x 2048  4.7 / 9.7;  2560 x 2560  6.1 / 9.6;  2560 x 4864  9.4 / 11.1;
+//                              9728 x 2560 13.3 / 11.6;  2560 x 9728 18.1 / 14.3;  1408 x 9728 16.5 / 12.4
+//                   32 tokens  1408 x 2048  5.0 / 10.0;  2560 x 2560  9.9 / 9.8;  4864 x 2560 13.0 / 11.1
 //   64 experts 1408 x 2048, ternary: 24 rows 14.4 / 20.3, 192 rows 32.5 / 35.6, 384 rows 41.6 / 36.1
 //   8 experts 4864 x 2560, 4-bit: 32 rows 29.7 / 30.2, 64 rows 39.2 / 32.9
-// Up to 8 tokens the weights meet one MMA tile of tokens.  Up to 16 the tensor path is behind
-// only while its blocks of 128 weight rows leave most SMs idle.
+// Up to 8 tokens the weights meet one MMA tile of tokens.  Beyond, the small path's time grows with
+// weights times chunks of 16 tokens, while the tensor path spreads few tiles over clusters.
 bool ep_is_small(int R, int E, int N, int K, bool grouped) {
   const int p = g_path.load();
   if (K > kEsMaxK) return false;
   if (p == TGEMM_PATH_TENSOR) return false;
   if (p != TGEMM_PATH_AUTO) return true;
   if (grouped) return R <= 16 || R <= 4 * E;
-  return R <= 8 || (R <= 16 && N < 6144);
+  return R <= 8 || (R <= 64 && static_cast<int64_t>((R + 15) / 16) * N * K <= 12 << 20);
 }
 
 int run_ep(const EpCall& c) {
@@ -217,7 +292,14 @@ int run_ep(const EpCall& c) {
   const size_t need = small ? 0 : ep_ws_bytes(c.R, c.K);
   if (need && (!c.workspace || c.ws_bytes < need)) return TGEMM_EWORKSPACE;
   if (need && !aligned(c.workspace, 256)) return TGEMM_EALIGN;
-  if (need && overlaps(c.y, y_bytes, c.workspace, need)) return TGEMM_EINVAL;
+  auto in_ws = [&](const void* p, size_t n) { return need && overlaps(c.workspace, need, p, n); };
+  if (in_ws(c.y, y_bytes) || in_ws(c.x, static_cast<size_t>(c.x_rows) * c.K * 2) ||
+      in_ws(c.wq, wrows * (c.K / (c.fmt == 0 ? 4 : 2))) ||
+      in_ws(c.scales, wrows * (c.fmt == 0 ? c.K / 128 * 2 : c.K / 64 * 4)) ||
+      in_ws(c.offsets, (static_cast<size_t>(c.E) + 1) * 4) || in_ws(c.rows, static_cast<size_t>(c.R) * 4) ||
+      in_ws(a.bias, static_cast<size_t>(c.E) * c.N * (a.bias_f32 ? 4 : 2)) ||
+      in_ws(a.gate, (a.gate_rows ? outs : c.N) * 2) || in_ws(a.residual, outs * (a.residual_f32 ? 4 : 2)))
+    return TGEMM_EINVAL;
   DeviceInfo di;
   if (int e = current_device_info(&di)) return e;
   const cudaStream_t st = as_stream(c.stream);
@@ -232,29 +314,18 @@ int run_ep(const EpCall& c) {
       }))
     return e;
 
-  const bool split = c.fmt == 1 && out_f32;
   EtParams p = {};
   p.N = c.N;
   p.K = c.K;
   p.E = c.E;
   p.R = c.R;
   p.tiles_n = (c.N + kEtRows - 1) / kEtRows;
-  const int most = out_f32 ? kEtSumTok : kEtTok;  // tokens of a tile
-  // Grouped: room for twice an expert's rows on average, of which 32 or 64 leave shared memory for
-  // more weights on their way (an expert with more rows takes more tiles).
-  const int64_t twice = 2 * static_cast<int64_t>(c.R) / c.E;
-  p.nt = !c.offsets ? et_pick_nt(c.R, p.tiles_n, most, di.sms) : twice <= 32 ? 32 : twice <= 64 ? 64 : most;
-  p.ksteps = split ? c.K / 64 : (c.K + 127) / 128;
   p.nblocks = c.K / (c.fmt == 0 ? 128 : 64);
   p.offsets = c.offsets;
   p.scales = c.scales;
   p.ep = a;
-  // the most tiles there can be: an expert with rows has at most one partly filled tile
-  const int64_t tiles = max_chunks(c.R, c.E, p.nt) * p.tiles_n;
-  if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
-  const int grid = static_cast<int>(std::min<int64_t>(tiles, di.sms));
-  if (c.fmt == 0) return out_f32 ? launch_ep_tc<0, false, true>(c, p, grid, st) : launch_ep_tc<0, false, false>(c, p, grid, st);
-  return split ? launch_ep_tc<1, true, true>(c, p, grid, st) : launch_ep_tc<1, false, false>(c, p, grid, st);
+  if (c.fmt == 0) return out_f32 ? launch_ep_tc<0, false, true>(c, p, di.sms, st) : launch_ep_tc<0, false, false>(c, p, di.sms, st);
+  return out_f32 ? launch_ep_tc<1, true, true>(c, p, di.sms, st) : launch_ep_tc<1, false, false>(c, p, di.sms, st);
 }
 
 // ---- expert sort and combine ---------------------------------------------------------------
@@ -291,6 +362,9 @@ int run_sort(const int* ids, int T, int k, int E, int* offsets, int* rows, int* 
   const size_t need = sort_workspace(n, E);
   if (need && (!workspace || ws_bytes < need)) return TGEMM_EWORKSPACE;
   if (need && !aligned(workspace, 256)) return TGEMM_EALIGN;
+  if (need && (overlaps(workspace, need, ids, nb) || overlaps(workspace, need, rows, nb) ||
+               overlaps(workspace, need, pos, nb) || overlaps(workspace, need, offsets, ob)))
+    return TGEMM_EINVAL;
   DeviceInfo di;
   if (int e = current_device_info(&di)) return e;
   static std::atomic<uint64_t> done{0};

@@ -71,11 +71,19 @@ struct EtFmt {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
+constexpr int kEtMaxSplit = 8;
+// The units [first, end) that CTA `rank` of a tile's `split` takes: whole pairs, since a pair of
+// ternary scales is one word.
+__host__ __device__ constexpr int et_first_unit(int ksteps, int split, int rank) {
+  return rank >= split ? ksteps : (ksteps + 1) / 2 * rank / split * 2;
+}
+
 struct EtParams {
   int N, K, E, R;
   int nt;                 // tokens per tile, a multiple of 16
   int tiles_n;            // ceil(N / 128)
   int ksteps;             // units of a tile: K / kBK, rounded up
+  int split;              // CTAs of a cluster that share a tile's units (dense calls)
   int nblocks;            // scale blocks of a row: K / 128 or K / 64
   const int* offsets;     // [E + 1] row ranges, or null: one expert, rows [0, R)
   const uint16_t* scales;
@@ -99,6 +107,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 // the map for a tile of mt tokens, and its box's rows
 __host__ __device__ constexpr int et_box(int mt) { return mt <= 16 ? 0 : mt <= 32 ? 1 : mt <= 64 ? 2 : 3; }
 __host__ __device__ constexpr int et_box_rows(int box, int nt) { return box < 3 ? 16 << box : nt; }
+
+// Every thread of a cluster, the warps each from where they are.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A store to shared memory of CTA `rank` of the cluster, at the place `addr` has in this one.
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(addr), "r"(rank), "f"(v)
+      : "memory");
+}
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -282,7 +302,7 @@ __device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
 // 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 48 steps the
 // epilogue warps take the accumulator into running sums in registers, rounded to nearest.  They
 // hold 80 tokens a tile.
-template <int FMT, bool SPLIT, bool SUMS>
+template <int FMT, bool SPLIT, bool SUMS, bool SHARE>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
   using F = EtFmt<FMT, SPLIT>;
@@ -357,7 +377,11 @@ __global__ void __launch_bounds__(kEtThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const EtTable tb{tab_off, tab_tp};
   const int num_tiles = tab_tp[p.E] * p.tiles_n;
-  const int ksteps = p.ksteps, nchunks = (ksteps + kCU - 1) / kCU;
+  // A cluster of p.split CTAs shares a tile: each has its own units and some of the outputs.
+  const int split = SHARE ? p.split : 1, rank = static_cast<int>(blockIdx.x) % split;
+  const int cta = static_cast<int>(blockIdx.x) / split, ctas = static_cast<int>(gridDim.x) / split;
+  const int ub0 = et_first_unit(p.ksteps, split, rank);
+  const int ksteps = et_first_unit(p.ksteps, split, rank + 1) - ub0, nchunks = (ksteps + kCU - 1) / kCU;
   constexpr int kAcc = SUMS ? kEtSumTok : kEtTok, kA0 = 2 * kEtTok;  // an accumulator's columns, the first A column
   // activation slots and weight stages
   const int lx = et_lx(p.nt, F::kBK), lw = et_lw(p.nt, F::kBK, F::kWBytes);
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       uint32_t it = 0;
       int e = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = cta; ok && t < num_tiles; t += ctas) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int box = et_box(tl.mt);
         const uint32_t bytes = 2u * F::kBK * et_box_rows(box, p.nt);
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           ok = et_wait(empty_bar(s), ((it >> lx) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(full_bar(s), bytes);
-          tma_load_3d(sbase + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, u * (F::kBK / 64));
+          tma_load_3d(sbase + s * xslot, &tm.x[box], full_bar(s), 0, tl.m0, (ub0 + u) * (F::kBK / 64));
         }
       }
       // every load issued must land before the CTA may exit
@@ -393,7 +417,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       uint32_t it = 0, sc = 0;  // units, accumulator segments
       int e = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = cta; ok && t < num_tiles; t += ctas) {
         const EtTile tl = et_tile(p, tb, t, e);
         const uint32_t ncols = static_cast<uint32_t>((tl.mt + 15) & ~15);
         const uint32_t idesc = make_idesc_f16(0u, kEtRows, ncols);
@@ -432,7 +456,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       uint32_t it = 0;
       int e = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < num_tiles; t += gridDim.x) {
+      for (int t = cta; ok && t < num_tiles; t += ctas) {
         const EtTile tl = et_tile(p, tb, t, e);
         const int row = tl.e * p.N + tl.n0;
         for (int u = 0; u < ksteps; ++u, ++it) {
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           ok = et_wait(wempty_bar(w), ((it >> lw) & 1u) ^ 1u, abort_flag);
           if (!ok) break;
           mbar_arrive_expect_tx(wfull_bar(w), F::kWBytes);
-          tma_load_2d(w_ring + w * F::kWBytes, &tm.w, wfull_bar(w), u * F::kWqRowBytes, row);
+          tma_load_2d(w_ring + w * F::kWBytes, &tm.w, wfull_bar(w), (ub0 + u) * F::kWqRowBytes, row);
         }
       }
       for (uint32_t j = (it > nw ? it - nw : 0); j < it; ++j) mbar_wait_drain(wfull_bar(j & (nw - 1)), (j >> lw) & 1u);
@@ -453,18 +477,19 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     // Asynchronous copies, as far ahead as the buffers go.
     constexpr int kW = F::kScWords, kR = 32 / kW;  // words of a row, rows a copy takes
     const int wd = lane % kW, rl = lane / kW;
+    const int kb0 = ub0 * kEtChunk / kCU;          // the first unit's block
     // pairs of Q2 scales are words only where the rows start on words
     const bool words = FMT == 1 || ((p.nblocks & 1) == 0 && (reinterpret_cast<uintptr_t>(p.scales) & 3) == 0);
     uint32_t cidx = 0;
     int e = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    for (int t = cta; t < num_tiles; t += ctas) {
       const EtTile tl = et_tile(p, tb, t, e);
       const int rows = min(kEtRows, p.N - tl.n0);
       const int64_t row0 = static_cast<int64_t>(tl.e) * p.N + tl.n0 + rl;
       for (int c = 0; c < nchunks; ++c, ++cidx) {
         const uint32_t b = cidx % kEtScBufs;
-        const int k = c * kEtChunk + wd * (kEtChunk / kW);  // the word's (first) block
+        const int k = kb0 + c * kEtChunk + wd * (kEtChunk / kW);  // the word's (first) block
         const uint32_t off = F::kScOff + b * F::kScBytes + wd * F::kScPitch + 4 * rl;
         ok = et_wait_warp(sempty_bar(b), ((cidx / kEtScBufs) & 1u) ^ 1u, abort_flag) && ok;
         if (!ok) continue;
@@ -508,8 +533,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     const uint8_t* s_mine = smem + F::kScOff + 4 * rt;
     // 16-byte chunk c of the row sits at chunk c ^ swz (TMA's 32- or 64-byte swizzle)
     const uint32_t swz = F::kWqRowBytes == 32 ? (rt >> 2) & 1 : (rt >> 1) & 3;
-    const int my_tiles = num_tiles > static_cast<int>(blockIdx.x)
-                             ? (num_tiles - static_cast<int>(blockIdx.x) + gridDim.x - 1) / gridDim.x : 0;
+    const int my_tiles = num_tiles > cta ? (num_tiles - cta + ctas - 1) / ctas : 0;
     uint32_t i = grp, i0 = 0, cidx = 0;  // the group's next unit; the chunk's first; chunks
     bool ok = true;
     for (int t = 0; t < my_tiles; ++t)
@@ -609,7 +633,7 @@ __global__ void __launch_bounds__(kEtThreads, 1)
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(accempty_bar(ab));
     };
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+    for (int t = cta; t < num_tiles; t += ctas) {
       const EtTile tl = et_tile(p, tb, t, e);
       const int n = tl.n0 + 32 * q + lane;       // this thread's weight row
       const bool nv = n < p.N;
@@ -766,20 +790,49 @@ __global__ void __launch_bounds__(kEtThreads, 1)
           ok = et_wait_warp(accfull_bar(ab), (sc >> 1) & 1u, abort_flag) && ok;
           tc_fence_after();
         };
-        if (set >= chunks) {
+        // Chunk cc of a shared tile belongs to CTA cc % split.  Once the cluster is done with its
+        // rings, each CTA puts its sums of the chunk there, and the owner adds them in CTA order.
+        const int first = rank + split * set, step = 2 * split;
+        const uint32_t part = 4u * (32 * q + lane);  // [chunk / split][CTA][16 tokens][128 rows]
+        if constexpr (SHARE) {
           accumulated();
-          release(ab);
-        }
-        for (int cc = set; cc < chunks; cc += 2) {
-          float f[16];
-          finish(f, 16 * cc, [&] {
-            if (cc == set) accumulated();  // the first chunk's operands are on their way already
+          cluster_sync();
+          for (int cc = set; cc < chunks; cc += 2) {
+            const int own = cc % split;
+            const uint32_t dst = sbase + part + 8192u * static_cast<uint32_t>(cc - own + rank);
             uint32_t v[16];
             tmem_ld_32x32b_x16(t_lane + ab * kAcc + 16 * cc, v);
             tmem_wait_ld();
-            if (cc + 2 >= chunks) release(ab);  // the accumulator is read out
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) st_cluster_f32(dst + 512u * i, own, __uint_as_float(v[i]));
+          }
+          cluster_sync();
+        }
+        if (first >= chunks) {
+          if (!SHARE) accumulated();
+          release(ab);
+        }
+        for (int cc = first; cc < chunks; cc += step) {
+          float f[16];
+          finish(f, 16 * cc, [&] {
+            if constexpr (SHARE) {
+              const float* src = reinterpret_cast<const float*>(smem + part + 8192u * static_cast<uint32_t>(cc - rank));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = src[128 * i];
+              for (int r = 1; r < split; ++r) {
+                src += 2048;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] += src[128 * i];
+              }
+            } else {
+              if (cc == set) accumulated();  // the first chunk's operands are on their way already
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(t_lane + ab * kAcc + 16 * cc, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
+            }
+            if (cc + step >= chunks) release(ab);  // the accumulator is read out
           });
         }
         ++sc;
@@ -789,6 +842,12 @@ __global__ void __launch_bounds__(kEtThreads, 1)
 
   // ------------------------------------------------------------ teardown
   __syncwarp();
+  // With the epilogue warps of the cluster: rings free, sums there.  (Each thread of a cluster
+  // comes to both barriers once: a split call has no more tiles than clusters.)
+  if (SHARE && (warp < kEtEpiWarp0 || cta >= num_tiles)) {
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -367,7 +367,7 @@ int tgemm_q4(const uint16_t* x, const uint8_t* wq, const uint16_t* sz, void* y, 
  *             (the other half of a gated MLP)
  *   residual  [M][N], f32 or bf16 by residual_dtype (16-byte aligned)
  * y may be the very tensor that residual is (of y's type), or that a bf16 gate[m][n] is; any
- * other overlap of y with an input or the workspace is refused (TGEMM_EINVAL).
+ * other overlap of y or the workspace with an input, or of the two, is refused (TGEMM_EINVAL).
  */
 typedef struct tgemm_epilogue {
   const void* bias;
@@ -381,11 +381,14 @@ typedef struct tgemm_epilogue {
 
 /*
  * tgemm_q2_ep, tgemm_q4_ep -- tgemm_q2 / tgemm_q4 with an epilogue (ep may be null: none).
- *   Operands, layouts and alignments as tgemm_q2 and tgemm_q4.  x must be finite with
- *   |x| < 65504.  Every scale is f32-applied or exact in the product's operands: a bf16 y of
- *   4-bit weights takes W as the f16 rounding of (q - z) * s, an f32 y takes it to f32.
- *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned; the call
- *   overwrites it, and calls sharing a workspace must not overlap on the GPU.
+ *   Operands, layouts and alignments as tgemm_q2 and tgemm_q4, N of at most 2^24
+ *   (TGEMM_ETOOLARGE beyond).  x must be finite with |x| < 65504: the tensor path multiplies
+ *   f16 copies of x, in which |x| below 2^-14 loses bits.  Ternary weights are exact.  The
+ *   tensor path takes 4-bit weights as f16(q * s - f16(z * s)) for a bf16 y, and as a high and
+ *   a low f16 part for an f32 y; the small path applies s and z in f32.  Sums are f32.
+ *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned, under the same
+ *   tgemm_set_path as the call (0, and workspace may be null, where the small path serves the
+ *   call); the call overwrites it, and calls sharing a workspace must not overlap on the GPU.
  *   wq and the scales are read before the wait for the kernels ahead on the stream, under
  *   the same rule as tgemm_q2; x, bias, gate and residual are read after it.
  */
@@ -430,7 +433,8 @@ size_t tgemm_grouped_workspace_size(int op, int R, int E, int N, int K);
  *   rows     int32 [T * k] out: the token of each sorted row; -1 behind the last
  *   pos      int32 [T][k] out: the sorted row of each pair; -1 for a pair left out
  *   workspace of tgemm_expert_sort_workspace_size(T, k, E) bytes (256-byte aligned; 0: none).
- *   All pointers 4-byte aligned; the outputs must not overlap each other or ids.
+ *   All pointers 4-byte aligned; the outputs and the workspace must not overlap each other or
+ *   ids.  The order does not depend on timing: the same ids give the same outputs.
  *   T * k of at most 2^26 (TGEMM_ETOOLARGE beyond).
  */
 int tgemm_expert_sort(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* rows, int32_t* pos,

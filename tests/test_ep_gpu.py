@@ -58,6 +58,44 @@ def test_odd_widths(path, pname, fmt, M, N, K, out):
     run(fmt, M, N, K, "none", "residual:f32", out, seed=K)
 
 
+@pytest.mark.parametrize("M,N,K", [(17, 128, 9728), (70, 72, 2176), (33, 301, 1152), (100, 250, 4096), (128, 640, 9728),
+                                   (40, 1408, 2048), (17, 2560, 2560), (130, 1279, 4224), (256, 2560, 9728)])
+@pytest.mark.parametrize("fmt,out", [("q2", "f32"), ("q2", "bf16"), ("q4", "f32"), ("q4", "bf16")])
+def test_few_tiles(path, M, N, K, fmt, out):
+    """Long rows and few tiles, whose units CTAs share: odd unit counts, ragged tiles, odd widths."""
+    path(tg.PATH_TENSOR)
+    run(fmt, M, N, K, "gelu", "bias:f32 gate:full residual:bf16", out, seed=K + M)
+
+
+@pytest.mark.parametrize("K", [1088, 3136])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_few_tiles_of_half_units(path, K, out):
+    path(tg.PATH_TENSOR)
+    run("q4", 50, 200, K, "none", "gate:row", out, seed=K)
+
+
+def test_few_tiles_repeat_and_replay(path):
+    """Shared tiles: the same bits each time, on two streams at once and from a graph."""
+    path(tg.PATH_TENSOR)
+    wq, sc, _ = pack("q2", (1408, 4096), 1, "cuda")
+    x = torch.randn(90, 4096, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    want = tg.gemm_q2_ep(x, wq, sc)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(20):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(tg.gemm_q2_ep(x, wq, sc))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=streams[0]):
+        kept = [tg.gemm_q2_ep(x, wq, sc) for _ in range(3)]
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, y) for y in got + kept)
+
+
 EPILOGUES = ["", "bias:bf16", "gate:row", "gate:full", "residual:bf16", "residual:f32", "bias:f32 gate:row residual:f32"]
 
 

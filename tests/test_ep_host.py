@@ -24,7 +24,7 @@ def ep(**kw):
 ep_keep = {}
 
 
-def call_ep(fn="tgemm_q2_ep", x=at(0), wq=at(1), sc=at(2), e=None, y=at(3), M=20, N=64, K=256, out=1, ws=at(4),
+def call_ep(fn="tgemm_q2_ep", x=at(0), wq=at(1), sc=at(2), e=None, y=at(3), M=96, N=64, K=256, out=1, ws=at(4),
             nbytes=MB, **_):
     return getattr(tg.lib(), fn)(x, wq, sc, e, y, M, N, K, out, ws, nbytes, None)
 
@@ -48,6 +48,9 @@ def call_grouped(fn="tgemm_q2_grouped", x=at(0), x_rows=20, wq=at(1), sc=at(2), 
     (dict(e=dict(gate=at(6) + 2)), tg.EALIGN), (dict(e=dict(residual=at(6) + 8)), tg.EALIGN),
     # y over an input: x, the weights, the workspace, a part of the residual, a residual or gate of another type or shape
     (dict(y=at(0) + 256), tg.EINVAL), (dict(y=at(1)), tg.EINVAL), (dict(y=at(2)), tg.EINVAL), (dict(y=at(4)), tg.EINVAL),
+    # the workspace over an input
+    (dict(ws=at(0)), tg.EINVAL), (dict(ws=at(1) + 256), tg.EINVAL), (dict(ws=at(2)), tg.EINVAL),
+    (dict(e=dict(bias=at(4))), tg.EINVAL), (dict(e=dict(gate=at(4) + 256)), tg.EINVAL), (dict(e=dict(residual=at(4))), tg.EINVAL),
     (dict(e=dict(residual=at(3) + 128, residual_dtype=1)), tg.EINVAL), (dict(e=dict(residual=at(3), residual_dtype=0)), tg.EINVAL),
     (dict(e=dict(gate=at(3), gate_rows=0)), tg.EINVAL), (dict(e=dict(gate=at(3) + 16, gate_rows=1)), tg.EINVAL),
     (dict(e=dict(gate=at(3), gate_rows=1), out=0), tg.EINVAL), (dict(e=dict(bias=at(3))), tg.EINVAL),
@@ -65,6 +68,7 @@ def test_ep_refuses(fn, kw, status):
     (dict(E=0), tg.EINVAL), (dict(E=1025), tg.EINVAL), (dict(off=at(5) + 2), tg.EALIGN), (dict(rows=at(6) + 1), tg.EALIGN),
     (dict(e=dict(gate=at(6), gate_rows=0)), tg.EINVAL), (dict(E=1024, N=2 ** 21), tg.ETOOLARGE),
     (dict(y=at(5)), tg.EINVAL), (dict(rows=at(6), y=at(6)), tg.EINVAL), (dict(nbytes=255), tg.EWORKSPACE),
+    (dict(ws=at(5)), tg.EINVAL), (dict(rows=at(4)), tg.EINVAL), (dict(ws=at(0)), tg.EINVAL),
 ], ids=str)
 def test_grouped_refuses(fn, kw, status):
     kw = dict(kw)
@@ -77,7 +81,8 @@ def test_grouped_refuses(fn, kw, status):
     (dict(ids=None), tg.EINVAL), (dict(T=0), tg.EINVAL), (dict(k=0), tg.EINVAL), (dict(E=0), tg.EINVAL), (dict(E=1025), tg.EINVAL),
     (dict(T=2 ** 26, k=2), tg.ETOOLARGE), (dict(T=2 ** 31 - 1, k=2 ** 31 - 1), tg.ETOOLARGE), (dict(ids=at(0) + 2), tg.EALIGN),
     (dict(rows=at(0)), tg.EINVAL), (dict(pos=at(2)), tg.EINVAL), (dict(off=at(3)), tg.EINVAL),
-    (dict(T=100000, ws=None), tg.EWORKSPACE), (dict(T=100000, nbytes=64), tg.EWORKSPACE), (dict(T=100000, ws=at(4) + 4), tg.EALIGN),
+    (dict(T=100000, ws=at(0)), tg.EINVAL), (dict(T=100000, ws=at(1)), tg.EINVAL), (dict(T=100000, rows=at(4)), tg.EINVAL),
+    (dict(T=100000, pos=at(4)), tg.EINVAL), (dict(T=100000, ws=None), tg.EWORKSPACE), (dict(T=100000, nbytes=64), tg.EWORKSPACE), (dict(T=100000, ws=at(4) + 4), tg.EALIGN),
 ], ids=str)
 def test_sort_refuses(kw, status):
     a = dict(ids=at(0), T=50, k=2, E=8, off=at(1), rows=at(2), pos=at(3), ws=at(4), nbytes=MB)
