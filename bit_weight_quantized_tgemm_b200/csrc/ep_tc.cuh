@@ -34,7 +34,7 @@ namespace tgemm {
 
 constexpr int kEtRows = 128;
 constexpr int kEtTok = 128;
-constexpr int kEtSumTok = 80;                   // most tokens of a tile with running sums
+constexpr int kEtSumTok = 96;                   // most tokens of a tile with running sums
 constexpr int kEtGroups = 3;                    // dequant groups of 4 warps, stages in turn
 constexpr int kEtWProdWarp = 2;
 constexpr int kEtScaleWarp = 3;
@@ -319,7 +319,7 @@ __device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
 // SUMS (f32 y): the tensor core adds each K = 16 step to the f32 accumulator with truncation,
 // 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 48 steps the
 // epilogue warps take the accumulator into running sums in registers, rounded to nearest.  They
-// hold 80 tokens a tile.
+// hold 96 tokens a tile.
 template <int FMT, bool SPLIT, bool SUMS, bool SHARE>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {
