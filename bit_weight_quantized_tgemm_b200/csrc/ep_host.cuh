@@ -135,7 +135,8 @@ int launch_ep_tc(const EpCall& c, EtParams p, int sms, cudaStream_t st) {
       }
       return n;
     });
-    p.nt = plan.nt;
+    const int tt = (c.R + plan.nt - 1) / plan.nt;
+    p.nt = ((c.R + tt - 1) / tt + 15) & ~15;  // the step that the kernel takes
     p.split = plan.split;
   }
   // the most tiles there can be: an expert with rows has at most one partly filled tile
@@ -147,9 +148,9 @@ int launch_ep_tc(const EpCall& c, EtParams p, int sms, cudaStream_t st) {
   EtMaps tm;
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   if (int e = encoder(&enc)) return e;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kEtBoxes; ++i) {
     // the boxes that tiles of up to nt tokens use; a dense call has full tiles and one rest
-    const int lo = i ? 8 << i : 0, hi = i < 3 ? 16 << i : kEtTok, rest = c.R % p.nt;
+    const int lo = i ? et_box_most(i - 1) : 0, hi = et_box_most(i), rest = c.R % p.nt;
     const bool used = c.offsets ? lo < p.nt : (c.R >= p.nt && p.nt > lo && p.nt <= hi) || (rest > lo && rest <= hi);
     if (!used) continue;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.R), static_cast<cuuint64_t>(c.K) / 64};

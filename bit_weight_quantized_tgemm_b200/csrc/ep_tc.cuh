@@ -109,9 +109,10 @@ struct EtParams {
 };
 
 // TMA maps.  Activations: the f16 copy as [k block of 64][row][64], boxes of a unit's one or two
-// k blocks and 16, 32, 64 or, for larger tiles, nt rows, so that one copy brings a tile's unit.
+// k blocks and 16, 32, 64, 96 or 128 rows (no more than nt), so that one copy brings a tile's unit.
+constexpr int kEtBoxes = 5;
 struct EtMaps {
-  CUtensorMap x[4];
+  CUtensorMap x[kEtBoxes];
   CUtensorMap w;
 };
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
@@ -123,8 +124,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 // the map for a tile of mt tokens, and its box's rows
-__host__ __device__ constexpr int et_box(int mt) { return mt <= 16 ? 0 : mt <= 32 ? 1 : mt <= 64 ? 2 : 3; }
-__host__ __device__ constexpr int et_box_rows(int box, int nt) { return box < 3 ? 16 << box : nt; }
+__host__ __device__ constexpr int et_box(int mt) { return mt <= 16 ? 0 : mt <= 32 ? 1 : (mt + 31) / 32; }
+__host__ __device__ constexpr int et_box_most(int box) { return box == 0 ? 16 : 32 * box; }
+__host__ __device__ constexpr int et_box_rows(int box, int nt) { return et_box_most(box) < nt ? et_box_most(box) : nt; }
+static_assert(et_box(kEtTok) == kEtBoxes - 1 && et_box(33) == 2 && et_box(64) == 2 && et_box(65) == 3, "boxes");
 
 // Every thread of a cluster, the warps each from where they are.
 __device__ __forceinline__ void cluster_sync() {
@@ -206,14 +209,15 @@ __device__ __forceinline__ int et_find(const int* tp, int E, int tt) {
 // Tile t of the walk (e is the walk's position, looked up again once t leaves that expert).
 __device__ __forceinline__ EtTile et_tile(const EtParams& p, const EtTable& tb, int t, int& e) {
   if (t >= tb.tp[e + 1] * p.tiles_n) e = et_find(tb.tp, p.E, t / p.tiles_n);
-  const int tt = tb.tp[e + 1] - tb.tp[e];
+  const int tt = tb.tp[e + 1] - tb.tp[e], rows = tb.off[e + 1] - tb.off[e];
+  const int step = ((rows + tt - 1) / tt + 15) & ~15;  // the rows in equal parts, as nt would make
   const int r = t - tb.tp[e] * p.tiles_n;
   const int tn = r / tt, ti = r - tn * tt;
   EtTile x;
   x.e = e;
   x.n0 = tn * kEtRows;
-  x.m0 = tb.off[e] + ti * p.nt;
-  x.mt = min(p.nt, tb.off[e + 1] - x.m0);
+  x.m0 = tb.off[e] + ti * step;
+  x.mt = min(step, tb.off[e + 1] - x.m0);
   return x;
 }
 
