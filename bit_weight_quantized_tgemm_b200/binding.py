@@ -406,6 +406,7 @@ class _Epilogue(ctypes.Structure):
 
 _pack_epilogue = struct.Struct("@PPPiiii").pack  # _Epilogue's bytes
 _bf16, _f16, _f32, _u8, _i32 = torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32
+_empty_like = torch.empty_like
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
@@ -462,13 +463,16 @@ def _epilogue(bias, act, gate, residual, M, N, index, E=None):
     return _pack_epilogue(pb, pg, pr, bias_dt, act, gate_rows, res_dt)
 
 
-def _result(y, like, M, N, out_dtype, index):
+def _result(y, like, M, N, out_dtype, index, residual=None):
     """The output tensor (a new one, or the caller's y) and its pointer."""
     if out_dtype != OUT_BF16 and out_dtype != OUT_F32:
         raise ValueError(f"out_dtype must be OUT_F32 or OUT_BF16, got {out_dtype}")
     dt = _bf16 if out_dtype == OUT_BF16 else _f32
     if y is None:
-        y = like.new_empty((M, N)) if like.dtype is dt else like.new_empty((M, N), dtype=dt)
+        if residual is not None and residual.dtype is dt:  # contiguous, of y's shape
+            y = _empty_like(residual)
+        else:
+            y = like.new_empty((M, N)) if like.dtype is dt else like.new_empty((M, N), dtype=dt)
         return y, y.data_ptr()
     ptr = _arg(y, dt, "y", index)
     _shape(y, (M, N), "y")
@@ -503,7 +507,7 @@ def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, 
     if bias is not None or act or gate is not None or residual is not None:
         ep = _epilogue(bias, act, gate, residual, M, N, index)
     L = _lib or lib()
-    y, py = _result(y, x, M, N, out_dtype, index)
+    y, py = _result(y, x, M, N, out_dtype, index, residual)
     ws, pws, nbytes = _call_workspace(L.tgemm_ep_workspace_size(op, M, N, K), workspace, x, index)
     st = getattr(L, fn)(x.data_ptr(), pw, ps, ep, py, M, N, K, out_dtype, pws, nbytes, _raw_stream(index))
     if st:
@@ -552,7 +556,7 @@ def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, r
     if bias is not None or act or gate is not None or residual is not None:
         ep = _epilogue(bias, act, gate, residual, R, N, index, E)
     L = _lib or lib()
-    y, py = _result(y, x, R, N, out_dtype, index)
+    y, py = _result(y, x, R, N, out_dtype, index, residual)
     ws, pws, nbytes = _call_workspace(L.tgemm_grouped_workspace_size(op, R, E, N, K), workspace, x, index)
     st = getattr(L, fn)(x.data_ptr(), x_rows, pw, ps, po, pr, ep, py, R, E, N, K, out_dtype, pws, nbytes,
                         _raw_stream(index))
@@ -598,7 +602,7 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     L = _lib or lib()
     offsets = ids.new_empty((experts + 1,))
     rows = ids.new_empty((T * k,))
-    pos = ids.new_empty((T, k))
+    pos = _empty_like(ids)
     ws, pws, nbytes = _call_workspace(L.tgemm_expert_sort_workspace_size(T, k, experts), workspace, ids, index)
     _check(L.tgemm_expert_sort(ids.data_ptr(), T, k, experts, offsets.data_ptr(), rows.data_ptr(),
                                pos.data_ptr(), pws, nbytes, _raw_stream(index)), "tgemm_expert_sort")
@@ -626,7 +630,7 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
         rd = _out_code(residual, "residual")
         pr = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (T, N), "residual")
-    y, py = _result(y, h, T, N, out_dtype, index)
+    y, py = _result(y, h, T, N, out_dtype, index, residual)
     _check(lib().tgemm_expert_combine(h.data_ptr(), hd, pp, pw, pr, rd, py, T, k, N, R, out_dtype,
                                       _raw_stream(index)), "tgemm_expert_combine")
     return y
