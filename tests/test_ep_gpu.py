@@ -1,4 +1,8 @@
 """Matmuls with an epilogue against their definition in 64 bits (GPU)."""
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -94,6 +98,30 @@ def test_few_tiles_repeat_and_replay(path):
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(want, y) for y in got + kept)
+
+
+def test_first_call_in_a_capture():
+    """A process whose first calls are captured: nothing in them may need to run before."""
+    code = """
+import torch
+import bit_weight_quantized_tgemm_b200 as tg
+wq = torch.zeros(1408, 512, dtype=torch.uint8, device="cuda")
+d = torch.ones(1408, 16, dtype=torch.float16, device="cuda")
+x = torch.ones(200, 2048, dtype=torch.bfloat16, device="cuda")
+ids = torch.zeros(3000, 2, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ys = [tg.gemm_q2_ep(x[:m], wq, d) for m in (1, 20, 100, 200)]
+    offsets, rows, pos = tg.expert_sort(ids, 4)
+g.replay()
+torch.cuda.synchronize()
+assert all((y == -2048).all() for y in ys)
+assert offsets.tolist() == [0, 6000, 6000, 6000, 6000]
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 EPILOGUES = ["", "bias:bf16", "gate:row", "gate:full", "residual:bf16", "residual:f32", "bias:f32 gate:row residual:f32"]
