@@ -224,6 +224,13 @@ __device__ __forceinline__ EtTile et_tile(const EtParams& p, const EtTable& tb, 
   return x;
 }
 
+// From L2: the line may be in this SM's L1 from an earlier call.
+__device__ __forceinline__ int ld_relaxed(const int* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // Group offsets come from the device and are not trusted: each is clamped to [previous, R],
 // so that every row range lies inside the caller's buffers.
 __device__ __forceinline__ void et_build_table(const int* offsets, int E, int R, int nt, int* off, int* tp) {
@@ -238,14 +245,14 @@ __device__ __forceinline__ void et_build_table(const int* offsets, int E, int R,
     return;
   }
   int tiles = 0;
-  int run = min(max(__ldg(offsets), 0), R);
+  int run = min(max(ld_relaxed(offsets), 0), R);
   if (lane == 0) {
     off[0] = run;
     tp[0] = 0;
   }
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    int v = e < E ? min(max(__ldg(offsets + e + 1), 0), R) : 0;
+    int v = e < E ? min(max(ld_relaxed(offsets + e + 1), 0), R) : 0;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, v, s);
@@ -391,9 +398,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     tmem_relinquish();
   }
   pdl_trigger();
-  // With device offsets every role needs them first; a dense call's weights are read early,
-  // and only the activation producer and the epilogue wait.
-  if (p.offsets || warp == 0 || warp >= kEtEpiWarp0) pdl_wait();
+  // Only the activation producer and the epilogue wait for the copy of x.  The weights are read
+  // early, and offsets come from before the copy's kernel, which waits for what is ahead of it
+  // before it lets this one start.
+  if (warp == 0 || warp >= kEtEpiWarp0) pdl_wait();
   if (warp == kEtWProdWarp) et_build_table(p.offsets, p.E, p.R, p.nt, tab_off, tab_tp);
   __syncwarp();
   tc_fence_before();
@@ -889,7 +897,12 @@ __global__ void __launch_bounds__(256) ep_prep_kernel(const uint16_t* __restrict
                                                       const int* __restrict__ rows,
                                                       const int* __restrict__ offsets, int E,
                                                       int x_rows, int R, int K) {
-  pdl_trigger_and_wait();
+  if (offsets) {
+    pdl_wait();  // the matmul reads the offsets as soon as it may start
+    pdl_trigger();
+  } else {
+    pdl_trigger_and_wait();
+  }
   const int lim = offsets ? min(max(__ldg(offsets + E), 0), R) : R;
   const int gk = K / 16;
   const int64_t total = static_cast<int64_t>(lim) * gk;
