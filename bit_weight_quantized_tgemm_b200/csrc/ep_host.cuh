@@ -173,22 +173,58 @@ int launch_ep_tc(const EpCall& c, EtParams p, int sms, cudaStream_t st) {
   });
 }
 
-template <int FMT, int T>
+constexpr int kEsMost = 225 * 1024, kEsHalf = 112 * 1024;  // shared memory of one CTA or two on an SM
+
+// CTAs that share the K of an item of the small path (a dense call with few items and long rows):
+// a warp's units take 0.6 to 1.4 us each, half more with two CTAs on an SM; meeting takes 1 us and
+// a little for each CTA (tenths of a us here).  Measured (us, chains of calls, by CTAs an item):
+//   1 x 1408 x 9728 ternary, 44 items: 1 8.7, 2 6.4, 3 5.8, 4 5.6, 6 6.5;  4-bit: 14.1, 8.1, 8.1, 7.1, 7.5
+//   1 x 2560 x 9728 ternary, 80 items: 1 9.1, 2 8.5, 3 7.8;  4-bit: 1 15.5, 3 9.7
+//   1 x 2560 x 2560 ternary, 80 items: 1 3.8, 2 4.4, 3 4.1
+int es_pick_split(int fmt, int T, int U, int64_t items, int sms) {
+  const int unit = T == 1 ? (fmt == 0 ? 6 : 9) : (fmt == 0 ? 11 : 14);
+  int best = 1, best_cost = 2 * unit * ((U + kEsWarps - 1) / kEsWarps);
+  for (int s = 2; s <= kEtMaxSplit; ++s) {
+    const int nu = (U + s * kEsWarps - 1) / (s * kEsWarps);
+    const int room = es_smem_bytes(fmt, T, true, nu, true, 1, false) <= kEsHalf ? 2 * sms : sms;
+    if (10 * items * s > 9 * room) continue;
+    const int cost = nu * unit * (items * s > sms ? 3 : 2) + 2 * (10 + 2 * s);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+template <int FMT, int T, bool SHARE>
 int launch_ep_small(EsParams p, int64_t chunks, int sms, cudaStream_t st) {
-  constexpr int kMost = 225 * 1024, kHalf = 112 * 1024;  // one CTA or two on an SM
   static std::atomic<uint64_t> done{0};
-  if (int e = allow_smem(ep_small_kernel<FMT, T>, kMost, done)) return e;
+  if (int e = allow_smem(ep_small_kernel<FMT, T, SHARE>, kEsMost, done)) return e;
   p.tiles_n = (p.N + kEsRows - 1) / kEsRows;
   const int64_t items = chunks * p.tiles_n;
   if (items > INT32_MAX / 2) return TGEMM_ETOOLARGE;
   const bool grouped = p.offsets != nullptr;
-  p.nu_max = (p.U + kEsWarps - 1) / kEsWarps;
-  p.staged = es_smem_bytes(FMT, T, p.nu_max, true, p.E, grouped) <= kMost ? 1 : 0;
-  const int smem = es_smem_bytes(FMT, T, p.nu_max, p.staged != 0, p.E, grouped);
-  if (smem > kMost) return TGEMM_ETOOLARGE;
-  const int grid = static_cast<int>(std::min<int64_t>(items, smem <= kHalf ? 2 * sms : sms));
+  p.nu_max = (p.U + p.split * kEsWarps - 1) / (p.split * kEsWarps);
+  p.staged = es_smem_bytes(FMT, T, SHARE, p.nu_max, true, p.E, grouped) <= kEsMost ? 1 : 0;
+  const int smem = es_smem_bytes(FMT, T, SHARE, p.nu_max, p.staged != 0, p.E, grouped);
+  if (smem > kEsMost) return TGEMM_ETOOLARGE;
+  const int grid = SHARE ? static_cast<int>(items) * p.split
+                         : static_cast<int>(std::min<int64_t>(items, smem <= kEsHalf ? 2 * sms : sms));
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(p.split), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = kEsWarps * 32;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = SHARE ? 2 : 1;
   return launch(FMT == 0 ? TGEMM_KIND_GEMV_Q2 : TGEMM_KIND_GEMV_Q4, st, [&] {
-    return pdl_launch(ep_small_kernel<FMT, T>, grid, kEsWarps * 32, static_cast<size_t>(smem), st, p);
+    return cudaLaunchKernelEx(&cfg, ep_small_kernel<FMT, T, SHARE>, p);
   });
 }
 
@@ -207,24 +243,27 @@ int run_ep_small(const EpCall& c, const EpArgs& a, int sms, cudaStream_t st) {
   p.rows = c.rows;
   p.ep = a;
   const int per = c.offsets ? (c.R + c.E - 1) / c.E : c.R;  // rows of an expert, on average
+  const int64_t chunks = max_chunks(c.R, c.E, per <= 8 ? 8 : 16);
+  p.split = c.offsets ? 1 : es_pick_split(c.fmt, per <= 8 ? 1 : 2, p.U, chunks * ((c.N + kEsRows - 1) / kEsRows), sms);
   auto go = [&](auto fmt_c) {
     constexpr int kF = decltype(fmt_c)::value;
-    if (per <= 8) return launch_ep_small<kF, 1>(p, max_chunks(c.R, c.E, 8), sms, st);
-    return launch_ep_small<kF, 2>(p, max_chunks(c.R, c.E, 16), sms, st);
+    if (p.split > 1)
+      return per <= 8 ? launch_ep_small<kF, 1, true>(p, chunks, sms, st) : launch_ep_small<kF, 2, true>(p, chunks, sms, st);
+    return per <= 8 ? launch_ep_small<kF, 1, false>(p, chunks, sms, st) : launch_ep_small<kF, 2, false>(p, chunks, sms, st);
   };
   return c.fmt == 0 ? go(std::integral_constant<int, 0>{}) : go(std::integral_constant<int, 1>{});
 }
 
 constexpr int kEsMaxK = 32768;  // a warp's scales of K fit in shared memory
-static_assert(es_smem_bytes(0, 2, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024 &&
-                  es_smem_bytes(1, 2, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024,
+static_assert(es_smem_bytes(0, 2, false, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024 &&
+                  es_smem_bytes(1, 2, false, kEsMaxK / 128 / kEsWarps, false, kEtMaxExperts, true) <= 225 * 1024,
               "shared memory of the small path");
 
 // Whether the small path serves a call; tgemm_set_path overrides it.  Measured in chains of calls
 // (us, small path / tensor path):
-//   dense, ternary   8 tokens  9728 x 2560  8.1 / 11.7;  2560 x 9728 10.4 / 14.2;  4-bit 16.0 / 15.4
-//                   16 tokens  1408 x 2048  4.7 / 9.7;  2560 x 2560  6.1 / 9.6;  2560 x 4864  9.4 / 11.1;
-//                              9728 x 2560 13.3 / 11.6;  2560 x 9728 18.1 / 14.3;  1408 x 9728 16.5 / 12.4
+//   dense, ternary   8 tokens  9728 x 2560  8.1 / 11.7;  2560 x 9728  8.6 / 14.2;  4-bit 10.0 / 15.4
+//                   16 tokens  1408 x 2048  4.7 / 9.7;  2560 x 2560  5.8 / 9.6;  2560 x 4864  8.3 / 11.1;
+//                              9728 x 2560 13.3 / 11.6;  2560 x 9728 18.1 / 14.3;  1408 x 9728  8.9 / 12.4
 //                   32 tokens  1408 x 2048  5.0 / 10.0;  2560 x 2560  9.9 / 9.8;  4864 x 2560 13.0 / 11.1
 //   64 experts 1408 x 2048, ternary: 24 rows 14.4 / 20.3, 192 rows 32.5 / 35.6, 384 rows 41.6 / 36.1
 //   8 experts 4864 x 2560, 4-bit: 32 rows 29.7 / 30.2, 64 rows 39.2 / 32.9
@@ -236,7 +275,7 @@ bool ep_is_small(int R, int E, int N, int K, bool grouped) {
   if (p == TGEMM_PATH_TENSOR) return false;
   if (p != TGEMM_PATH_AUTO) return true;
   if (grouped) return R <= 16 || R <= 4 * E;
-  return R <= 8 || (R <= 64 && static_cast<int64_t>((R + 15) / 16) * N * K <= 12 << 20);
+  return R <= 8 || (R <= 64 && static_cast<int64_t>((R + 15) / 16) * N * K <= 14 << 20);
 }
 
 int run_ep(const EpCall& c) {

@@ -26,6 +26,8 @@
 // us in a chain of calls (0.4 TB/s), of which 3 us are there at any size; 8 tokens x 9728 x 2560
 // ternary 8.1 us (0.8 TB/s), where unpacking and the MMAs of 8-token tiles fill the issue slots.
 // The 4-bit fragments are twice as many bytes and 1.4 times the instructions: 12.0 us (1.1 TB/s).
+// A warp's units follow each other at 0.6 to 1.4 us, so that long rows with few items go to
+// clusters (SHARE): one token x 1408 x 9728 4-bit 14.1 -> 6.5 us.
 #pragma once
 
 #include "common.cuh"
@@ -44,6 +46,7 @@ struct EsParams {
   int U;        // units of 128 k
   int tiles_n;  // blocks of 32 weight rows
   int nu_max;   // most units of a warp
+  int split;    // CTAs of a cluster that share an item's K (dense calls)
   int staged;   // activations kept in shared memory (else read from global each unit)
   const uint16_t* x;
   const uint8_t* wq;
@@ -55,11 +58,14 @@ struct EsParams {
 
 // Scale words of a row that a warp's units can take: Q2 two blocks a word, 4-bit two words a unit.
 __host__ __device__ constexpr int es_words(int fmt, int nu) { return (fmt == 0 ? nu / 2 + 1 : 2 * nu) + 3 & ~3; }
-__host__ __device__ constexpr int es_red_bytes(int T) { return 2 * kEsWarps * 8 * T * kEsPitch * 4; }
+// two buffers of the warps' sums, or one and the sums of a cluster's CTAs
+__host__ __device__ constexpr int es_red_bytes(int T, bool share) {
+  return (kEsWarps * kEsPitch + (share ? kEtMaxSplit * kEsRows : kEsWarps * kEsPitch)) * 8 * T * 4;
+}
 __host__ __device__ constexpr int es_scale_bytes(int fmt, int nu) { return kEsWarps * 2 * es_words(fmt, nu) * 128; }
 __host__ __device__ constexpr int es_x_bytes(int T, int nu) { return kEsWarps * nu * T * 2048; }
-__host__ __device__ constexpr int es_smem_bytes(int fmt, int T, int nu, bool staged, int E, bool grouped) {
-  return es_red_bytes(T) + es_scale_bytes(fmt, nu) + (staged ? es_x_bytes(T, nu) : 0) + (grouped ? 2 * (E + 2) * 4 : 0);
+__host__ __device__ constexpr int es_smem_bytes(int fmt, int T, bool share, int nu, bool staged, int E, bool grouped) {
+  return es_red_bytes(T, share) + es_scale_bytes(fmt, nu) + (staged ? es_x_bytes(T, nu) : 0) + (grouped ? 2 * (E + 2) * 4 : 0);
 }
 
 __device__ __forceinline__ uint2 ld_stream_v2(const uint8_t* p) {
@@ -84,7 +90,8 @@ struct EsUnit {
   uint32_t w[4][kW];
 };
 
-template <int FMT, int T>
+// SHARE: the warps of a cluster's CTAs share the K of one item; CTA 0 adds the CTAs' sums in order.
+template <int FMT, int T, bool SHARE>
 __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsParams p) {
   constexpr int kTok = 8 * T;
   constexpr int kUnitBytes = FMT == 0 ? 32 : 64;
@@ -95,7 +102,7 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   float* red = reinterpret_cast<float*>(es_smem);  // [buffer][warp][token][kEsPitch]
   const int words = es_words(FMT, p.nu_max);
-  uint8_t* sc_base = es_smem + es_red_bytes(T);
+  uint8_t* sc_base = es_smem + es_red_bytes(T, SHARE);
   uint4* sc_mine = reinterpret_cast<uint4*>(sc_base) + warp * 2 * words * 8;   // [buffer][word][8 g][4 j]
   uint4* xs_mine = reinterpret_cast<uint4*>(sc_base + es_scale_bytes(FMT, p.nu_max)) +
                    warp * p.nu_max * T * 128 + lane;                            // [unit][tile][4][lane]
@@ -104,9 +111,13 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
   int* tab_tp = tab_off + p.E + 2;
   const int row_bytes = FMT == 0 ? p.K / 4 : p.K / 2;
   const int nscale = FMT == 0 ? p.K / 128 : p.K / 64;
-  const int ua = p.U * warp / kEsWarps, ub = p.U * (warp + 1) / kEsWarps, nu = ub - ua;
+  const int split = SHARE ? p.split : 1, rank = static_cast<int>(blockIdx.x) % split;
+  const int cta = static_cast<int>(blockIdx.x) / split, ctas = static_cast<int>(gridDim.x) / split;
+  const int part = rank * kEsWarps + warp, parts = split * kEsWarps;
+  const int ua = p.U * part / parts, ub = p.U * (part + 1) / parts, nu = ub - ua;
 
   pdl_trigger();
+  if (SHARE) cluster_arrive();  // CTA 0 is there to be written to
   int num_items;
   const int chunks = (p.R + kTok - 1) / kTok;  // dense
   if (p.offsets) {
@@ -118,8 +129,8 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
     num_items = chunks * p.tiles_n;
   }
   // this CTA's items
-  const int t0 = static_cast<int>(static_cast<int64_t>(num_items) * blockIdx.x / gridDim.x);
-  const int t1 = static_cast<int>(static_cast<int64_t>(num_items) * (blockIdx.x + 1) / gridDim.x);
+  const int t0 = static_cast<int>(static_cast<int64_t>(num_items) * cta / ctas);
+  const int t1 = static_cast<int>(static_cast<int64_t>(num_items) * (cta + 1) / ctas);
   struct Item {
     int e, n0, m0, mt;
   };
@@ -374,7 +385,32 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
           rb[(warp * kTok + 8 * i + 2 * c + (k & 1)) * kEsPitch + 16 * h + g + 8 * (k >> 1)] = acc[h][i][k];
     __syncthreads();
     const int n = cur.n0 + lane;
-    if (n < p.N) {
+    if constexpr (SHARE) {
+      // the only item; CTA 0 gets the sums [CTA][token][32 rows]
+      float* all = red + kEsWarps * kTok * kEsPitch;
+      cluster_wait();
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const int m = warp + kEsWarps * i;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEsWarps; ++w) v += rb[(w * kTok + m) * kEsPitch + lane];
+        st_cluster_f32(smem_u32(all + (rank * kTok + m) * kEsRows + lane), 0, v);
+      }
+      cluster_sync();
+      if (rank > 0) break;
+      if (n < p.N) {
+        float bias = 0.f;
+        if (p.ep.bias) bias = ep_load(p.ep.bias, n, p.ep.bias_f32);
+        for (int m = warp; m < cur.mt; m += kEsWarps) {
+          float v[1] = {0.f};
+          for (int r = 0; r < split; ++r) v[0] += all[(r * kTok + m) * kEsRows + lane];
+          v[0] += bias;
+          ep_act_all(v, p.ep.act);
+          ep_store1(p.ep, cur.m0 + m, n, p.N, v[0]);
+        }
+      }
+    } else if (n < p.N) {
       float bias = 0.f;
       if (p.ep.bias) bias = ep_load(p.ep.bias, static_cast<int64_t>(cur.e) * p.N + n, p.ep.bias_f32);
 #pragma unroll
@@ -391,6 +427,10 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
     }
     cur = nxt;
     wcur = wnxt;
+  }
+  if (SHARE && t0 >= t1) {  // each thread of a cluster comes to both barriers
+    cluster_wait();
+    cluster_sync();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }

@@ -133,8 +133,11 @@ __host__ __device__ constexpr int et_box_rows(int box, int nt) { return et_box_m
 static_assert(et_box(kEtTok) == kEtBoxes - 1 && et_box(33) == 2 && et_box(64) == 2 && et_box(65) == 3, "boxes");
 
 // Every thread of a cluster, the warps each from where they are.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // A store to shared memory of CTA `rank` of the cluster, at the place `addr` has in this one.
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v) {

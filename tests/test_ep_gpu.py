@@ -71,6 +71,19 @@ def test_few_tiles(path, M, N, K, fmt, out):
     run(fmt, M, N, K, "gelu", "bias:f32 gate:full residual:bf16", out, seed=K + M)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 512, 9728), (3, 1408, 9728), (8, 41, 5120), (16, 300, 9728), (13, 1408, 4096), (1, 2560, 9728),
+                                   (40, 70, 9728)])
+@pytest.mark.parametrize("fmt,out", [("q2", "f32"), ("q2", "bf16"), ("q4", "f32"), ("q4", "bf16")])
+def test_few_items(path, M, N, K, fmt, out):
+    """Few rows, few weight rows and long K, which CTAs share; twice the same bits."""
+    path(tg.PATH_SMALL_M)
+    run(fmt, M, N, K, "silu", "bias:bf16 gate:full residual:f32", out, seed=K + M)
+    wq, sc, _ = pack(fmt, (N, K), 9, "cuda")
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    ys = [fn(fmt)(x, wq, sc) for _ in range(5)]
+    assert all(torch.equal(ys[0], y) for y in ys)
+
+
 @pytest.mark.parametrize("K", [1088, 3136])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_few_tiles_of_half_units(path, K, out):
