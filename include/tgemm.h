@@ -384,8 +384,9 @@ typedef struct tgemm_epilogue {
  *   Operands, layouts and alignments as tgemm_q2 and tgemm_q4, N of at most 2^24
  *   (TGEMM_ETOOLARGE beyond).  x must be finite with |x| < 65504: the tensor path multiplies
  *   f16 copies of x, in which |x| below 2^-14 loses bits.  Ternary weights are exact.  The
- *   tensor path takes 4-bit weights as f16(q * s - f16(z * s)) for a bf16 y, and as a high and
- *   a low f16 part for an f32 y; the small path applies s and z in f32.  Sums are f32.
+ *   tensor path takes 4-bit weights as f16((q - c) * s - f16((z - c) * s)) for a bf16 y, c the
+ *   whole number next to z (no further from (q - z) * s than its f16 rounding after that of
+ *   q - z, as in tgemm_q4), and as a high and a low f16 part for an f32 y; the small path applies s and z in f32.  Sums are f32.
  *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned, under the same
  *   tgemm_set_path as the call (0, and workspace may be null, where the small path serves the
  *   call); the call overwrites it, and calls sharing a workspace must not overlap on the GPU.
