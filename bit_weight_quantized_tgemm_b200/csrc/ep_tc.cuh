@@ -351,13 +351,15 @@ __device__ __forceinline__ bool q4_zero_exact(uint32_t z16) {
   return (z >= 7.f && z <= 8.f) || (z >= 0.f && z <= 16.f && z128 == rintf(z128));
 }
 
-// SPLIT (4-bit weights, f32 y): a unit's weights are a high and a low f16 part in two A stages,
-// since f16 weights alone are 2^-12 relative off.
+// SPLIT (4-bit weights, f32 y): a unit's weights are a high and a low f16 part in one A stage,
+// since f16 weights alone are 2^-12 relative off.  The low part is subnormal for weights below
+// 2^-3 and so off by up to 2^-25: y is 1e-6 off with scales around 0.01, 4e-5 with 0.0001.  (One
+// power of two over all weights would shift that floor, but only at the cost of large weights.)
 //
 // SUMS (f32 y): the tensor core adds each K = 16 step to the f32 accumulator with truncation,
 // 1.5e-8 of the sum per step towards zero (2.3e-6 at K = 2560), so after every 48 steps the
-// epilogue warps take the accumulator into running sums in registers, rounded to nearest.  They
-// hold 96 tokens a tile.
+// epilogue warps take the accumulator into running sums in registers, rounded to nearest: 5e-7 of
+// the norm of y at K = 2560, 6.7e-7 at 9728.  They hold 96 tokens a tile.
 template <int FMT, bool SPLIT, bool SUMS, bool SHARE>
 __global__ void __launch_bounds__(kEtThreads, 1)
     ep_tc_kernel(const __grid_constant__ EtMaps tm, const EtParams p) {

@@ -42,7 +42,7 @@
  * Accuracy: the matmuls accumulate in f32.  The tensor-core path multiplies f16
  * operands: x is converted bf16 -> f16 (exact for |x| in f16's normal range; x must be
  * finite with |x| < 65504), Q2 weights (q-1)*d are exact in f16, 4-bit weights are the
- * f16 rounding of (q - z) * s.
+ * f16 rounding of (q - z) * s (other forms of them: tgemm_q4_ep).
  */
 #ifndef TGEMM_H
 #define TGEMM_H
@@ -383,10 +383,14 @@ typedef struct tgemm_epilogue {
  * tgemm_q2_ep, tgemm_q4_ep -- tgemm_q2 / tgemm_q4 with an epilogue (ep may be null: none).
  *   Operands, layouts and alignments as tgemm_q2 and tgemm_q4, N of at most 2^24
  *   (TGEMM_ETOOLARGE beyond).  x must be finite with |x| < 65504: the tensor path multiplies
- *   f16 copies of x, in which |x| below 2^-14 loses bits.  Ternary weights are exact.  The
- *   tensor path takes 4-bit weights as f16((q - c) * s - f16((z - c) * s)) for a bf16 y, c the
- *   whole number next to z (no further from (q - z) * s than its f16 rounding after that of
- *   q - z, as in tgemm_q4), and as a high and a low f16 part for an f32 y; the small path applies s and z in f32.  Sums are f32.
+ *   f16 copies of x, in which |x| below 2^-14 loses bits.  Sums are f32.  Ternary weights are
+ *   exact.  The small path applies 4-bit scales and zero points in f32.  The tensor path takes
+ *   4-bit weights
+ *     for a bf16 y  as f16((q - c) * s - f16((z - c) * s)), c the whole number next to z: no
+ *                   further off than f16(f16(q - z) * s), the weights of tgemm_q4
+ *     for an f32 y  as a high and a low f16 part, off by at most 2^-22 of the weight and, where
+ *                   the low part is subnormal, 2^-25: scales around 1e-2, 1e-3 and 1e-4 give y to
+ *                   1e-6, 4e-6 and 4e-5 of its norm
  *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned, under the same
  *   tgemm_set_path as the call (0, and workspace may be null, where the small path serves the
  *   call); the call overwrites it, and calls sharing a workspace must not overlap on the GPU.

@@ -148,3 +148,40 @@ def test_ternary_weights_up_to_the_f16_range(path, pname, out):
     bound = (K / 16 + K / 64) * 2.0 ** -23 * (x.double().abs() @ w2.abs().T)
     bound = bound + (2.0 ** -24 if out == tg.OUT_F32 else 2.0 ** -8) * (ref.abs() + bound)
     assert ((y.double() - ref).abs() <= bound).all()
+
+
+# The tensor core cuts each K = 16 step's sum off, by 1.5e-8 (2^-26) of it on average, and running sums
+# are taken every 48 steps, so that a segment's partial sums grow as the root of the steps: the cuts
+# come to 2 / 3 * 48 * 2^-26 of the segment, and, the segments' signs being independent, of y.  Twice
+# that is allowed.  One accumulator for all of K would be 2.3e-6 off at K = 2560 and 8e-6 at 9728.
+SUMS = 2 * (2 / 3 * 48) * 2.0 ** -26
+
+
+@pytest.mark.parametrize("pname", list(PATHS))
+@pytest.mark.parametrize("M,K", [(20, 2560), (130, 2560), (20, 9728), (130, 9728), (60, 9664)])
+@pytest.mark.parametrize("fmt,size", [("q2", 0.02), ("q2", 0.0002), ("q4", 0.01), ("q4", 0.001), ("q4", 0.0001)])
+def test_f32_y(path, pname, M, K, fmt, size):
+    """f32 outputs, for ordinary and small scales.  4-bit weights are two f16 parts on the tensor path:
+    the low one is off by at most 2^-22 |w| and where it is subnormal by 2^-25, whatever the scale."""
+    if fmt == "q2" and K % 128:
+        K += 64
+    path(PATHS[pname])
+    N = 136
+    wq, sc, w = pack(fmt, (N, K), K + M, "cuda")
+    f = size / (0.02 if fmt == "q2" else 0.01)
+    if fmt == "q2":
+        sc = (sc.float() * f).half()
+        w = w.sign() * sc.double().repeat_interleave(128, -1)
+    else:
+        q = (w / sc[..., 0].double().repeat_interleave(64, -1) + sc[..., 1].double().repeat_interleave(64, -1)).round()
+        sc[..., 0] = (sc[..., 0].float() * f).half()
+        w = (q - sc[..., 1].double().repeat_interleave(64, -1)) * sc[..., 0].double().repeat_interleave(64, -1)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(K)).bfloat16().cuda()
+    ref = x.double() @ w.T
+    y = (tg.gemm_q2_ep if fmt == "q2" else tg.gemm_q4_ep)(x, wq, sc, out_dtype=tg.OUT_F32)
+    torch.cuda.synchronize()
+    low = 0.0
+    if fmt == "q4" and pname == "tensor":
+        low = float(((x.double() ** 2) @ (((2.0 ** -22 * w) ** 2 + 2.0 ** -50) / 3).T).sum()) ** 0.5
+    got, bound = float((y.double() - ref).norm()), float(ref.norm()) * (SUMS + 2.0 ** -24) + low
+    assert got <= bound, f"{got / float(ref.norm()):.3g} of the norm, at most {bound / float(ref.norm()):.3g}"
