@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
           cp_async4(smem_u32(d), src, 4u);
         } else {
           const uint16_t* src = p.scales + row * nscale + 2 * (wbase + w);
-          uint32_t v = __ldg(src);
-          if (2 * (wbase + w) + 1 < nscale) v |= static_cast<uint32_t>(__ldg(src + 1)) << 16;
+          uint32_t v = ld_scale(src);
+          if (2 * (wbase + w) + 1 < nscale) v |= static_cast<uint32_t>(ld_scale(src + 1)) << 16;
           *d = v;
         }
       }
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
     const uint4* xs = reinterpret_cast<const uint4*>(src);
     uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
     if (ok) {
-      r0 = __ldg(xs);
-      r1 = __ldg(xs + 1);
+      r0 = xs[0];
+      r1 = xs[1];
     }
     const uint32_t r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
 #pragma unroll
       for (int i = 0; i < T; ++i) {
         int64_t m = cur.m0 + min(g + 8 * i, cur.mt - 1);
-        if (p.rows) m = __ldg(p.rows + m);
+        if (p.rows) m = p.rows[m];
         xok[i] = m >= 0 && m < p.x_rows;  // else a row of zeros
         xp[i] = p.x + (xok[i] ? m : 0) * p.K + static_cast<int64_t>(ua) * 128 + (FMT == 0 ? 32 : 16) * c;
       }

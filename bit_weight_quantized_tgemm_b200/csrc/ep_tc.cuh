@@ -570,8 +570,8 @@ __global__ void __launch_bounds__(kEtThreads, 1)
             uint32_t v = 0u;
             if (r + rl < rows) {
               const uint16_t* src = p.scales + (row0 + r) * p.nblocks + k;
-              if (k < p.nblocks) v = __ldg(src);
-              if (k + 1 < p.nblocks) v |= static_cast<uint32_t>(__ldg(src + 1)) << 16;
+              if (k < p.nblocks) v = ld_scale(src);
+              if (k + 1 < p.nblocks) v |= static_cast<uint32_t>(ld_scale(src + 1)) << 16;
             }
             *reinterpret_cast<uint32_t*>(smem + off + 4 * r) = v;
           }
@@ -918,18 +918,15 @@ __global__ void __launch_bounds__(kEtThreads, 1)
 // The f16 copy of the activations in the dequantizers' k order, row by row: row r of the copy
 // is row rows[r] of x (or r), for the rows some expert has; an index outside x gives zeros.
 template <int FMT>
-__global__ void __launch_bounds__(256) ep_prep_kernel(const uint16_t* __restrict__ x,
-                                                      uint16_t* __restrict__ x16,
-                                                      const int* __restrict__ rows,
-                                                      const int* __restrict__ offsets, int E,
-                                                      int x_rows, int R, int K) {
+__global__ void __launch_bounds__(256) ep_prep_kernel(const uint16_t* x, uint16_t* x16, const int* rows,
+                                                      const int* offsets, int E, int x_rows, int R, int K) {
   if (offsets) {
     pdl_wait();  // the matmul reads the offsets as soon as it may start
     pdl_trigger();
   } else {
     pdl_trigger_and_wait();
   }
-  const int lim = offsets ? min(max(__ldg(offsets + E), 0), R) : R;
+  const int lim = offsets ? min(max(offsets[E], 0), R) : R;
   const int gk = K / 16;
   const int64_t total = static_cast<int64_t>(lim) * gk;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -937,12 +934,12 @@ __global__ void __launch_bounds__(256) ep_prep_kernel(const uint16_t* __restrict
     const int64_t r = i / gk;
     const int g = static_cast<int>(i - r * gk);
     int64_t src = r;
-    if (rows) src = __ldg(rows + r);
+    if (rows) src = rows[r];
     uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
     if (src >= 0 && src < x_rows) {
       const uint4* xp = reinterpret_cast<const uint4*>(x + src * K) + 2 * g;
-      a = __ldg(xp);
-      b = __ldg(xp + 1);
+      a = xp[0];
+      b = xp[1];
     }
     x16_group<FMT>(a, b, reinterpret_cast<uint4*>(x16 + r * K) + 2 * g);
   }

@@ -17,6 +17,12 @@ struct EpArgs {
   int bias_f32, gate_rows, residual_f32, out_f32, act;
 };
 
+// What another kernel may have written just before (activations, plans, epilogue operands) is read by
+// ordinary loads after the wait for that kernel: this grid may be resident while it is written,
+// and the read-only path is for memory that nobody writes meanwhile.  Packed weights and scales,
+// which are read ahead of the wait, take the read-only path.
+__device__ __forceinline__ uint16_t ld_scale(const uint16_t* p) { return __ldg(p); }
+
 __device__ __forceinline__ float ep_exp2(float t) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
@@ -62,8 +68,7 @@ __device__ __forceinline__ void ep_act_all(float (&v)[n], int act) {
 }
 
 __device__ __forceinline__ float ep_load(const void* p, int64_t i, int f32) {
-  return f32 ? __ldg(static_cast<const float*>(p) + i)
-             : bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p) + i));
+  return f32 ? static_cast<const float*>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
 }
 
 // gate and residual of one element, and its store.  The residual is read with a plain load:
