@@ -407,8 +407,9 @@ class _Epilogue(ctypes.Structure):
 _pack_epilogue = struct.Struct("@PPPiiii").pack  # _Epilogue's bytes
 _bf16, _f16, _f32, _u8, _i32 = torch.bfloat16, torch.float16, torch.float32, torch.uint8, torch.int32
 _empty_like = torch.empty_like
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# a torch without CUDA has neither; every call has then refused its tensors before it needs them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _on_device(index: int, call):
