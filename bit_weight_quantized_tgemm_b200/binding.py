@@ -441,6 +441,12 @@ def _out_code(t, name: str) -> int:
     raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor, got {dt or type(t).__name__}")
 
 
+def _c_ints(where: str, *sizes):
+    """Refuses sizes that a C int does not hold (ctypes would pass their low 32 bits)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise TgemmError(ETOOLARGE, where)
+
+
 def _shape(t: torch.Tensor, shape, name: str):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -502,6 +508,7 @@ def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, 
         raise ValueError("x and wq must have two dimensions")
     M, K = x.shape
     N = wq.shape[0]
+    _c_ints(fn, M, N, K)
     _shape(wq, (N, K // per_byte), "wq")
     _shape(sc, (N, K // 128) if per_byte == 4 else (N, K // 64, 2), "scales")
     ep = None
@@ -553,6 +560,7 @@ def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, r
         if rows.dim() != 1:
             raise ValueError("rows must have one dimension")
         R = rows.shape[0]
+    _c_ints(fn, x_rows, R, E, N, K)
     ep = None
     if bias is not None or act or gate is not None or residual is not None:
         ep = _epilogue(bias, act, gate, residual, R, N, index, E)
@@ -600,6 +608,7 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     if experts < 1 or experts > MAX_EXPERTS:
         raise ValueError(f"experts must be 1 to {MAX_EXPERTS}, got {experts}")
     T, k = ids.shape
+    _c_ints("tgemm_expert_sort", T, k)
     L = _lib or lib()
     offsets = ids.new_empty((experts + 1,))
     rows = ids.new_empty((T * k,))
@@ -625,6 +634,7 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
         raise ValueError("h must be [R, N] and pos [T, k]")
     T, k = pos.shape
     R, N = h.shape
+    _c_ints("tgemm_expert_combine", T, k, R, N)
     _shape(weights, (T, k), "weights")
     rd, pr = 0, None
     if residual is not None:
