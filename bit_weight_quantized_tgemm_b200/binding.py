@@ -516,6 +516,8 @@ def _gemm_ep(fn, op, x, wq, sc, per_byte, bias, act, gate, residual, out_dtype, 
         ep = _epilogue(bias, act, gate, residual, M, N, index)
     L = _lib or lib()
     y, py = _result(y, x, M, N, out_dtype, index, residual)
+    if M == 0:
+        return y
     ws, pws, nbytes = _call_workspace(L.tgemm_ep_workspace_size(op, M, N, K), workspace, x, index)
     st = getattr(L, fn)(x.data_ptr(), pw, ps, ep, py, M, N, K, out_dtype, pws, nbytes, _raw_stream(index))
     if st:
@@ -529,7 +531,7 @@ def gemm_q2_ep(x, wq, d, *, bias=None, act: int = ACT_NONE, gate=None, residual=
 
     bias f32 or bf16 [N]; act ACT_*; gate bf16 [N] or [M, N]; residual f32 or bf16 [M, N].  The
     epilogue is f32 with one rounding, at the store.  y may be the residual (of y's type) or a
-    bf16 [M, N] gate.  See tgemm_epilogue in tgemm.h."""
+    bf16 [M, N] gate.  An x of no rows gives an empty y.  See tgemm_epilogue in tgemm.h."""
     return _gemm_ep("tgemm_q2_ep", OP_Q2, x, wq, d, 4, bias, act, gate, residual, out_dtype, y, workspace)
 
 
@@ -566,6 +568,8 @@ def _gemm_grouped(fn, op, x, wq, sc, per_byte, offsets, rows, bias, act, gate, r
         ep = _epilogue(bias, act, gate, residual, R, N, index, E)
     L = _lib or lib()
     y, py = _result(y, x, R, N, out_dtype, index, residual)
+    if R == 0:
+        return y
     ws, pws, nbytes = _call_workspace(L.tgemm_grouped_workspace_size(op, R, E, N, K), workspace, x, index)
     st = getattr(L, fn)(x.data_ptr(), x_rows, pw, ps, po, pr, ep, py, R, E, N, K, out_dtype, pws, nbytes,
                         _raw_stream(index))
@@ -581,7 +585,7 @@ def gemm_q2_grouped(x, wq, d, offsets, *, rows=None, bias=None, act: int = ACT_N
 
     wq uint8 [E, N, K/4], d f16 [E, N, K/128], offsets int32 [E+1] on the device (as expert_sort
     gives them), rows int32 [R]; bias [E, N], gate bf16 [R, N], residual [R, N].  Rows of y behind
-    the last group are left as they were.  See tgemm_q2_grouped in tgemm.h."""
+    the last group are left as they were; R = 0 gives an empty y.  See tgemm_q2_grouped in tgemm.h."""
     return _gemm_grouped("tgemm_q2_grouped", OP_Q2, x, wq, d, 4, offsets, rows, bias, act, gate, residual,
                          out_dtype, y, workspace)
 
@@ -599,7 +603,7 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     Returns (offsets int32 [experts+1], rows int32 [T*k], pos int32 [T, k]): expert e's sorted
     rows are [offsets[e], offsets[e+1]), rows[r] is the token of sorted row r (-1 behind the
     last), pos[t, j] the sorted row of pair (t, j) (-1 for an id outside [0, experts), whose pair
-    is left out).  Pairs of one expert keep their order."""
+    is left out).  Pairs of one expert keep their order.  No tokens give a plan of no rows."""
     index = _first(ids, _i32, "ids")
     if _current_device() != index:
         return _on_device(index, lambda: expert_sort(ids, experts, workspace=workspace))
@@ -613,6 +617,8 @@ def expert_sort(ids: torch.Tensor, experts: int, *, workspace=None):
     offsets = ids.new_empty((experts + 1,))
     rows = ids.new_empty((T * k,))
     pos = _empty_like(ids)
+    if T == 0:
+        return offsets.zero_(), rows, pos
     ws, pws, nbytes = _call_workspace(L.tgemm_expert_sort_workspace_size(T, k, experts), workspace, ids, index)
     _check(L.tgemm_expert_sort(ids.data_ptr(), T, k, experts, offsets.data_ptr(), rows.data_ptr(),
                                pos.data_ptr(), pws, nbytes, _raw_stream(index)), "tgemm_expert_sort")
@@ -623,7 +629,7 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
                    out_dtype: int = OUT_BF16, y=None):
     """y[t] = residual[t] + sum_j weights[t, j] * h[pos[t, j]] (pairs with pos outside [0, R) left
     out): h f32 or bf16 [R, N], pos int32 [T, k], weights f32 [T, k], residual f32 or bf16 [T, N].
-    f32 sums in the order of j."""
+    f32 sums in the order of j.  No tokens give an empty y."""
     hd = _out_code(h, "h")
     index = _first(h, h.dtype, "h")
     if _current_device() != index:
@@ -642,6 +648,8 @@ def expert_combine(h: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor, *,
         pr = _arg(residual, residual.dtype, "residual", index)
         _shape(residual, (T, N), "residual")
     y, py = _result(y, h, T, N, out_dtype, index, residual)
+    if T == 0:
+        return y
     _check(lib().tgemm_expert_combine(h.data_ptr(), hd, pp, pw, pr, rd, py, T, k, N, R, out_dtype,
                                       _raw_stream(index)), "tgemm_expert_combine")
     return y
