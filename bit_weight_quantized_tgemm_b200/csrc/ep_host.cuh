@@ -142,6 +142,7 @@ int launch_ep_tc(const EpCall& c, EtParams p, int sms, cudaStream_t st) {
   // the most tiles there can be: an expert with rows has at most one partly filled tile
   const int64_t tiles = max_chunks(c.R, c.E, p.nt) * p.tiles_n;
   if (tiles > INT32_MAX / 2) return TGEMM_ETOOLARGE;
+  // a shared call has exactly one cluster a tile: the kernel's cluster barriers count on it
   attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
   cfg.numAttrs = p.split > 1 ? 2 : 1;
   cfg.gridDim = static_cast<unsigned>(p.split > 1 ? tiles * p.split : std::min<int64_t>(tiles, sms));
@@ -209,6 +210,7 @@ int launch_ep_small(EsParams p, int64_t chunks, int sms, cudaStream_t st) {
   p.staged = es_smem_bytes(FMT, T, SHARE, p.nu_max, true, p.E, grouped) <= kEsMost ? 1 : 0;
   const int smem = es_smem_bytes(FMT, T, SHARE, p.nu_max, p.staged != 0, p.E, grouped);
   if (smem > kEsMost) return TGEMM_ETOOLARGE;
+  // shared items: exactly one cluster each, which the kernel's cluster barriers count on
   const int grid = SHARE ? static_cast<int>(items) * p.split
                          : static_cast<int>(std::min<int64_t>(items, smem <= kEsHalf ? 2 * sms : sms));
   cudaLaunchAttribute attr[2] = {};

@@ -386,7 +386,8 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
     __syncthreads();
     const int n = cur.n0 + lane;
     if constexpr (SHARE) {
-      // the only item; CTA 0 gets the sums [CTA][token][32 rows]
+      // the cluster's only item (the grid has one cluster for each); CTA 0 gets the sums
+      // [CTA][token][32 rows]
       float* all = red + kEsWarps * kTok * kEsPitch;
       cluster_wait();
 #pragma unroll
@@ -427,10 +428,6 @@ __global__ void __launch_bounds__(kEsWarps * 32, 2) ep_small_kernel(const EsPara
     }
     cur = nxt;
     wcur = wnxt;
-  }
-  if (SHARE && t0 >= t1) {  // each thread of a cluster comes to both barriers
-    cluster_wait();
-    cluster_sync();
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }

@@ -424,9 +424,10 @@ __global__ void __launch_bounds__(kEtThreads, 1)
     tmem_relinquish();
   }
   pdl_trigger();
-  // Only the activation producer and the epilogue wait for the copy of x.  The weights are read
-  // early, and offsets come from before the copy's kernel, which waits for what is ahead of it
-  // before it lets this one start.
+  // The activation producer and the epilogue wait for the copy of x, and the barrier below for
+  // them, so that the other roles too start behind the copy.  Only the experts' table is built
+  // meanwhile: offsets come from before the copy's kernel, which waits for what is ahead of it before
+  // it lets this one start.
   if (warp == 0 || warp >= kEtEpiWarp0) pdl_wait();
   if (warp == kEtWProdWarp) et_build_table(p.offsets, p.E, p.R, p.nt, tab_off, tab_tp);
   __syncwarp();
@@ -901,9 +902,9 @@ __global__ void __launch_bounds__(kEtThreads, 1)
 
   // ------------------------------------------------------------ teardown
   __syncwarp();
-  // With the epilogue warps of the cluster: rings free, sums there.  (Each thread of a cluster
-  // comes to both barriers once: a split call has no more tiles than clusters.)
-  if (SHARE && (warp < kEtEpiWarp0 || cta >= num_tiles)) {
+  // With the epilogue warps of the cluster: rings free, sums there.  Each thread of a cluster comes
+  // to both barriers once: the grid of a shared call has one cluster for each tile.
+  if (SHARE && warp < kEtEpiWarp0) {
     cluster_sync();
     cluster_sync();
   }

@@ -28,9 +28,10 @@ __device__ __forceinline__ float ep_exp2(float t) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
-// v / (1 + 2^-t), from the exponential and quotient units: the exponential is within 2^-22 and the
-// quotient within 2 f32 steps, and a denominator past 2^126 gives 0, as v * 2^-126 would round
-// to for any v of use.
+// v / (1 + 2^-t), from the exponential and quotient units: the exponential is within 2^-22, the
+// quotient within 2 f32 steps, and the rounding of t, at most 2^-24 of it, moves the exponential by
+// 2^-24 ln(2) |t|: for v below 0 in all up to 1.5e-6 of the result at v = -20, where that is 4e-8,
+// and 5e-6 at v = -87.  A denominator past 2^126 gives 0: results below 1e-36 are flushed.
 // 1536 x 9472 x 1280 ternary with a tanh GELU: 56 us with expf, 50 us.
 __device__ __forceinline__ float ep_logistic(float v, float t) { return __fdividef(v, 1.f + ep_exp2(-t)); }
 

@@ -64,7 +64,9 @@ extern "C" {
 #define TGEMM_EWORKSPACE -5 /* workspace missing or smaller than tgemm_workspace_size_min() */
 #define TGEMM_ETOOLARGE  -6 /* tgemm_q2_noalloc: the problem needs more scratch than its
                                built-in buffer (TGEMM_NOALLOC_SCRATCH_BYTES) holds;
-                               q2_from_gemlite: more than 2^31 - 1 transpose tiles */
+                               q2_from_gemlite: more than 2^31 - 1 transpose tiles;
+                               epilogue and expert calls: more weight rows, outputs or pairs
+                               than they take */
 
 /* ---- output element types ---------------------------------------------------------- */
 #define TGEMM_OUT_F32  0
@@ -386,16 +388,17 @@ typedef struct tgemm_epilogue {
  *   f16 copies of x, in which |x| below 2^-14 loses bits.  Sums are f32.  Ternary weights are
  *   exact.  The small path applies 4-bit scales and zero points in f32.  The tensor path takes
  *   4-bit weights
- *     for a bf16 y  as f16((q - c) * s - f16((z - c) * s)), c the whole number next to z: no
- *                   further off than f16(f16(q - z) * s), the weights of tgemm_q4
+ *     for a bf16 y  as f16((q - c) * s - f16((z - c) * s)), c the whole number next to z: as
+ *                   near in all as f16(f16(q - z) * s), the weights of tgemm_q4
  *     for an f32 y  as a high and a low f16 part, off by at most 2^-22 of the weight and, where
  *                   the low part is subnormal, 2^-25: scales around 1e-2, 1e-3 and 1e-4 give y to
  *                   1e-6, 4e-6 and 4e-5 of its norm
  *   workspace: tgemm_ep_workspace_size(op, M, N, K) bytes, 256-byte aligned, under the same
  *   tgemm_set_path as the call (0, and workspace may be null, where the small path serves the
  *   call); the call overwrites it, and calls sharing a workspace must not overlap on the GPU.
- *   wq and the scales are read before the wait for the kernels ahead on the stream, under
- *   the same rule as tgemm_q2; x, bias, gate and residual are read after it.
+ *   wq and the scales may be read before the wait for the kernels ahead on the stream (the
+ *   small path of tgemm_q2_ep and tgemm_q4_ep does so), under the same rule as tgemm_q2; x, bias,
+ *   gate and residual are read after it.
  */
 int tgemm_q2_ep(const uint16_t* x, const uint8_t* wq, const uint16_t* d, const tgemm_epilogue* ep, void* y, int M,
                 int N, int K, int out_dtype, void* workspace, size_t ws_bytes, void* stream);
