@@ -22,10 +22,11 @@
 //   ternary  acc += d * sum (q - 1) x
 //   4-bit    acc += s * (sum (q - 8) x - (z - 8) sum x)
 //
-// What bounds it: latency, then instructions.  One token x 2560 x 2560 ternary, 1.8 MB, takes 4.1
-// us in a chain of calls (0.4 TB/s), of which 3 us are there at any size; 8 tokens x 9728 x 2560
-// ternary 8.1 us (0.8 TB/s), where unpacking and the MMAs of 8-token tiles fill the issue slots.
-// The 4-bit fragments are twice as many bytes and 1.4 times the instructions: 12.0 us (1.1 TB/s).
+// What bounds it: latency.  One token x 2560 x 2560 ternary, 1.8 MB, takes 4.1 us in a chain of calls
+// (0.4 TB/s), of which 3 us are there at any size; 8 tokens x 9728 x 2560 ternary 7.9 us
+// (0.8 TB/s), 4-bit 10.7 us (1.3 TB/s, twice the bytes).  Counters of these two, cold: 39 and 37 % of
+// the issue slots used, ALU 28 %, tensor pipe 10 and 12 %, and the warps wait for global loads more
+// than for anything else (3.2 and 2.7 warps for each instruction issued).
 // A warp's units follow each other at 0.6 to 1.4 us, so that long rows with few items go to
 // clusters (SHARE): one token x 1408 x 9728 4-bit 14.1 -> 6.5 us.
 #pragma once

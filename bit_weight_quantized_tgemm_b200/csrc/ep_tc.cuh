@@ -21,9 +21,12 @@
 // the MMA thread's waits and issue (some 460 cycles) beside it; a fourth group, units of 64 k
 // or tests of the barriers ahead of the waits change nothing or cost.  A unit of 128 tokens
 // takes 0.45 us or 790 cycles, of which the tensor core is busy for 512 (1536 x 12288 x 2560
-// ternary, 82 us: 1180 TFLOP/s, tensor pipe 61 %, 11 TB/s out of L2).  It is not L2: pairs of CTAs
+// ternary, 81 us in a replayed graph: 1190 TFLOP/s, tensor pipe 68 % of active cycles, 11 TB/s out
+// of L2).  It is not L2: pairs of CTAs
 // that each load half of the tokens take 80 us.  The dequantizers' stores and the accumulators
-// share tensor memory, and the issue slots are 59 % full.  About 8 us a call are the copy of x, the
+// share tensor memory, and the issue slots are 66 % full.  The kernels are held to 80 registers a
+// thread and spill: 20 to 48 bytes for a bf16 y, 260 to 280 for an f32 one, whose running sums take
+// 48 registers of the epilogue's threads.  About 8 us a call are the copy of x, the
 // start of both kernels, the first unit and the last epilogue (148 tiles of 17 tokens x 16 units:
 // 13.0 us; five rounds of them 33.9 us).
 #pragma once
